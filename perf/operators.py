@@ -98,7 +98,7 @@ def draw(rng):
         heads = k_heads * rng.choice([1, 1, 2, 3, 4])
         most = MOST_TOKEN_HEADS // (8 if op == "train" else 1)
         seqs = _spread(rng, 1, 40)
-        hi = _spread(rng, 1, 8192 if op == "scan" else 2048)
+        hi = _spread(rng, 1, 8192) if op == "scan" else _spread(rng, 24, 2048)
         while seqs * hi * heads > most:
             if seqs > 1:
                 seqs -= max(1, seqs // 4)
