@@ -281,6 +281,94 @@ int seed_dense_step(const seed_dims* dims, float* S, int32_t layer, const float*
                     const float* k, const float* v, const float* alpha, const float* beta,
                     float* o, void* ws, size_t ws_bytes, void* stream);
 
+/* ---- Whole sequences on dense states.  What leaves the dense states a conversion
+ * starts from (SEED figures & tables, Figure 1(a): the prefill), and its gradients.
+ *
+ * Sequences lie packed one behind the other: sequence s holds the rows
+ * offsets[s] .. offsets[s+1] - 1 of the per-token arrays, and may be empty.  Rows
+ * outside every sequence are neither read nor written.  Offsets are on the device; an
+ * entry outside [0, tokens] or behind its successor raises SEED_FLAG_BADINDEX and makes
+ * its sequence an empty one (what the rows of the other sequences of such a call
+ * receive is unspecified; nothing outside the arrays is touched).                     */
+typedef struct {
+  int32_t form;     /* seed_form */
+  int32_t seqs;     /* sequences, >= 1 */
+  int32_t heads;    /* heads H (of v, the decays, the states) */
+  int32_t k_heads;  /* heads of q and k; divides heads: head h reads key head h / (heads / k_heads) */
+  int32_t d_k;      /* as in seed_dims */
+  int32_t d_v;
+  int32_t max_len;  /* the longest sequence's tokens: decides which kernels run, not what they compute */
+  int32_t elem;     /* seed_factors: element type of q, k, v, o and of their gradients */
+  int64_t tokens;   /* rows of the per-token arrays, >= 0 and below 2^31 */
+} seed_scan_dims;
+
+/* Bytes of device workspace the two calls below need (status words and scratch; the
+ * scratch is written anew by every call, so calls on one stream may share it).
+ * 0 for unsupported dims.  Initialise with seed_workspace_init before first use.     */
+size_t seed_scan_workspace_bytes(const seed_scan_dims* dims, int32_t backward);
+
+/* seed_dense_step over every token of every sequence, from the state S0:
+ *     S' = Diag(a) S,  w = beta (v - S'^T k) (Mamba-2: Delta v),  S = S' + k w^T,  o = S^T q
+ * which is seed_dense_step's recurrence, a being the form's decay.
+ *   offsets [seqs+1] int32     q, k [tokens][k_heads][d_k]     v, o [tokens][heads][d_v]
+ *   alpha   [tokens][heads], KDA [tokens][heads][d_k]          beta [tokens][heads]
+ *   S0      [seqs][heads][d_k][d_v] float32, or NULL for zeros
+ *   S_out   the same, or NULL: the states behind the last tokens; may be S0 itself
+ * alpha and beta are float32.  Decays enter as products (never as quotients or
+ * logarithms), so any finite alpha is allowed, zero included.  All states and sums are
+ * float32; o is rounded once.  With d_k and d_v from the other calls, S_out is one
+ * layer's S_dense for seed_state_init_from_dense.                                   */
+int seed_dense_scan(const seed_scan_dims* dims, const int32_t* offsets, const void* q, const void* k,
+                    const void* v, const float* alpha, const float* beta, const float* S0, void* o,
+                    float* S_out, void* ws, size_t ws_bytes, void* stream);
+
+/* Gradients of seed_dense_scan: from d_o = dL/do [tokens][heads][d_v] (element type
+ * elem) and dS_out = dL/dS_out (float32, or NULL for zeros) those of every input,
+ *   dq, dk [tokens][k_heads][d_k] (sums over the heads that share a key head),
+ *   dv [tokens][heads][d_v] (element type elem), dbeta as beta (float32),
+ *   dlog_alpha as alpha (float32): dL/d(log alpha) = alpha dL/d(alpha), which stays
+ *   finite at alpha = 0 (it is 0 there; like every sum here it is accurate to float32
+ *   of the terms it sums, not of a small difference of theirs), and
+ *   dS0 [seqs][heads][d_k][d_v] float32, or NULL; may be dS_out itself.
+ * The forward's states are recomputed; nothing is kept from the forward call.  Results
+ * do not depend on the order in which blocks run (no atomic sums).                   */
+int seed_dense_scan_backward(const seed_scan_dims* dims, const int32_t* offsets, const void* q,
+                             const void* k, const void* v, const float* alpha, const float* beta,
+                             const void* d_o, const float* S0, const float* dS_out, void* dq, void* dk,
+                             void* dv, float* dlog_alpha, float* dbeta, float* dS0, void* ws,
+                             size_t ws_bytes, void* stream);
+
+/* ---- Drafted tokens.  A tree of tokens proposed for one request, all read against
+ * the stored state in one call: node t continues node parent[t], the nodes with parent
+ * -1 the stored state itself.  The state is not changed.
+ *   n_nodes N <= SEED_MAX_NODES, the same for all requests
+ *   parent [B][N] int32, parent[b][t] < t; below -1: the node is unused
+ *   q, k [B][N][H][d_k]   v, o, w [B][N][H][d_v]
+ *   alpha  [B][N][H], KDA [B][N][H][d_k]   beta [B][N][H]
+ * o[t] is what seed_decode_step returns for token t after the steps of its ancestors;
+ * w[t] the value that token writes, S_t = S'_t + k_t w_t^T (needed by the commit).
+ * Unused nodes get zeros.  A parent >= t raises SEED_FLAG_BADINDEX; that node and the
+ * nodes below it count as unused.  A node reads its own ancestors only: non-finite
+ * values of one branch stay in it.  SEED_FLAG_BADCOLS: a column count outside
+ * [0, R+W]; that unit's o and w are not written.                                     */
+#define SEED_MAX_NODES 64
+int seed_decode_tree(const seed_dims* dims, const seed_state* state, int32_t layer, int32_t n_nodes,
+                     const int32_t* parent, const float* q, const float* k, const float* v,
+                     const float* alpha, const float* beta, float* o, float* w, void* ws,
+                     size_t ws_bytes, void* stream);
+
+/* Takes the path from the stored state to node leaf[b] (int32 [B]) of a tree that
+ * seed_decode_tree has read into the stored state: what seed_decode_step would leave
+ * after the path's tokens in turn (each appends one column pair).  parent, k, v, alpha,
+ * beta as given to seed_decode_tree, w as it returned it.  leaf[b] < 0: nothing was
+ * accepted, the request's units stay as they are.  Units are left unchanged under
+ * SEED_FLAG_FULL (the path needs more columns than R+W leaves: compress first),
+ * SEED_FLAG_BADINDEX (leaf is no used node), SEED_FLAG_BADCOLS, SEED_FLAG_ZERO_VBAR.   */
+int seed_decode_tree_commit(const seed_dims* dims, const seed_state* state, int32_t layer,
+                            int32_t n_nodes, const int32_t* parent, const int32_t* leaf, const float* k,
+                            const float* v, const float* alpha, const float* beta, const float* w,
+                            void* ws, size_t ws_bytes, void* stream);
+
 /* Synchronises `stream`, returns the accumulated SEED_FLAG_* bits in *flags and
  * clears them.  Returns SEED_OK or SEED_ERR_CUDA.                                   */
 int seed_get_status(void* ws, void* stream, uint32_t* flags);

@@ -23,6 +23,7 @@ Modules:
   bytes_model  the analytical byte account (Table 17) behind Table 2
   precision    rounding to the 16-bit factor formats (Table 9)
   diagnostics  sink and content energies (Figures 3 and 12)
+  sequence     whole sequences, their gradients, and trees of drafted tokens
   run          whole trajectories (prefill, convert, decode, compress) for sampled units
 
 Parity pins: every function above is pinned in tests/test_oracle_pins.py to a
@@ -31,4 +32,4 @@ recurrence, Lemma 1's sink recurrence, Eckart-Young by brute force, Corollary 4,
 the delta-rule write, closed-form unrolled sums, Table 2's byte values).
 """
 
-from . import bytes_model, compress, convert, diagnostics, factored, precision, recurrences, run  # noqa: F401
+from . import bytes_model, compress, convert, diagnostics, factored, precision, recurrences, run, sequence  # noqa: F401

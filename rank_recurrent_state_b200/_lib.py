@@ -28,6 +28,11 @@ class seed_state(ctypes.Structure):
                 ("ncols", c_void_p), ("vbar", c_void_p)]
 
 
+class seed_scan_dims(ctypes.Structure):
+    _fields_ = [("form", c_int32), ("seqs", c_int32), ("heads", c_int32), ("k_heads", c_int32), ("d_k", c_int32),
+                ("d_v", c_int32), ("max_len", c_int32), ("elem", c_int32), ("tokens", ctypes.c_int64)]
+
+
 class seed_synth_key(ctypes.Structure):
     _fields_ = [("seed", c_uint32), ("workload", c_uint32), ("vbar_unit", c_int32), ("b0", c_int32)]
 
@@ -60,6 +65,14 @@ SIGNATURES = {
     "seed_dense_step": (ctypes.c_int, [ctypes.POINTER(seed_dims), c_void_p, c_int32, c_void_p, c_void_p,
                                        c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_size_t,
                                        c_void_p]),
+    "seed_scan_workspace_bytes": (c_size_t, [ctypes.POINTER(seed_scan_dims), c_int32]),
+    "seed_dense_scan": (ctypes.c_int, [ctypes.POINTER(seed_scan_dims)] + [c_void_p] * 10 + [c_size_t, c_void_p]),
+    "seed_dense_scan_backward": (ctypes.c_int, [ctypes.POINTER(seed_scan_dims)] + [c_void_p] * 16
+                                 + [c_size_t, c_void_p]),
+    "seed_decode_tree": (ctypes.c_int, [ctypes.POINTER(seed_dims), ctypes.POINTER(seed_state), c_int32, c_int32]
+                         + [c_void_p] * 9 + [c_size_t, c_void_p]),
+    "seed_decode_tree_commit": (ctypes.c_int, [ctypes.POINTER(seed_dims), ctypes.POINTER(seed_state), c_int32, c_int32]
+                                + [c_void_p] * 8 + [c_size_t, c_void_p]),
     "seed_get_status": (ctypes.c_int, [c_void_p, c_void_p, ctypes.POINTER(c_uint32)]),
     "seed_get_diagnostics": (ctypes.c_int, [c_void_p, c_void_p, ctypes.POINTER(c_uint32)]),
     "seed_status_string": (ctypes.c_char_p, [ctypes.c_int]),

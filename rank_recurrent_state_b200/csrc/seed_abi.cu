@@ -56,6 +56,27 @@ int check_state(const seed_state* s) {
   return SEED_OK;
 }
 
+int check_scan_dims(const seed_scan_dims* d) {
+  if (!d) return SEED_ERR_INVALID_ARG;
+  if (d->form < SEED_GDN || d->form > SEED_MAMBA2) return SEED_ERR_INVALID_ARG;
+  if (d->elem < SEED_FACTORS_F32 || d->elem > SEED_FACTORS_BF16) return SEED_ERR_INVALID_ARG;
+  if (d->seqs < 1 || d->heads < 1 || d->k_heads < 1 || d->tokens < 0 || d->max_len < 0) return SEED_ERR_INVALID_ARG;
+  if (d->heads % d->k_heads) return SEED_ERR_SHAPE;
+  if (!seed::decode_dims_supported(d->d_k, d->d_v)) return SEED_ERR_SHAPE;
+  if (d->tokens > 0x7fffffffLL) return SEED_ERR_SHAPE;
+  // one block per (sequence, head, 32 value columns) and per (chunk slot, head)
+  const long long slots = d->tokens / 64 + d->seqs;
+  if (slots > 0x7fffffffLL / d->heads || (long long)d->seqs * d->heads > 0x7fffffffLL / 4) return SEED_ERR_SHAPE;
+  return SEED_OK;
+}
+
+int check_tree(const seed_dims* d, int32_t layer, int32_t n_nodes) {
+  if (const int rc = check_dims(d)) return rc;
+  if (const int rc = check_layer(d, layer, false)) return rc;
+  if (n_nodes < 1) return SEED_ERR_INVALID_ARG;
+  return n_nodes <= SEED_MAX_NODES ? SEED_OK : SEED_ERR_SHAPE;
+}
+
 #define SEED_TRY(x)          \
   do {                       \
     const int rc_ = (x);     \
@@ -238,6 +259,95 @@ int seed_dense_step(const seed_dims* dims, float* S, int32_t layer, const float*
   SEED_TRY(check_ws(ws, ws_bytes));
   return seed::launch_dense_step(*dims, S, layer, q, k, v, alpha, beta, o, status_word(ws),
                                  as_stream(stream));
+}
+
+size_t seed_scan_workspace_bytes(const seed_scan_dims* dims, int32_t backward) {
+  if (check_scan_dims(dims)) return 0;
+  return seed::scan_workspace_bytes(*dims, backward != 0);
+}
+
+int seed_dense_scan(const seed_scan_dims* dims, const int32_t* offsets, const void* q, const void* k, const void* v,
+                    const float* alpha, const float* beta, const float* S0, void* o, float* S_out, void* ws,
+                    size_t ws_bytes, void* stream) {
+  SEED_TRY(check_scan_dims(dims));
+  SEED_TRY(check_ptr(offsets));
+  if (dims->tokens > 0) {      // the arrays of no tokens may be null
+    SEED_TRY(check_ptr(q));
+    SEED_TRY(check_ptr(k));
+    SEED_TRY(check_ptr(v));
+    SEED_TRY(check_ptr(alpha));
+    SEED_TRY(check_ptr(beta));
+    SEED_TRY(check_ptr(o));
+  }
+  SEED_TRY(check_opt_ptr(S0));
+  SEED_TRY(check_opt_ptr(S_out));
+  SEED_TRY(check_ws(ws, ws_bytes));
+  if (ws_bytes < seed::scan_workspace_bytes(*dims, false)) return SEED_ERR_WORKSPACE;
+  return seed::launch_scan(*dims, offsets, q, k, v, alpha, beta, S0, o, S_out, ws, as_stream(stream));
+}
+
+int seed_dense_scan_backward(const seed_scan_dims* dims, const int32_t* offsets, const void* q, const void* k,
+                             const void* v, const float* alpha, const float* beta, const void* d_o, const float* S0,
+                             const float* dS_out, void* dq, void* dk, void* dv, float* dlog_alpha, float* dbeta,
+                             float* dS0, void* ws, size_t ws_bytes, void* stream) {
+  SEED_TRY(check_scan_dims(dims));
+  SEED_TRY(check_ptr(offsets));
+  if (dims->tokens > 0) {
+    SEED_TRY(check_ptr(q));
+    SEED_TRY(check_ptr(k));
+    SEED_TRY(check_ptr(v));
+    SEED_TRY(check_ptr(alpha));
+    SEED_TRY(check_ptr(beta));
+    SEED_TRY(check_ptr(d_o));
+    SEED_TRY(check_ptr(dq));
+    SEED_TRY(check_ptr(dk));
+    SEED_TRY(check_ptr(dv));
+    SEED_TRY(check_ptr(dlog_alpha));
+    SEED_TRY(check_ptr(dbeta));
+  }
+  SEED_TRY(check_opt_ptr(S0));
+  SEED_TRY(check_opt_ptr(dS_out));
+  SEED_TRY(check_opt_ptr(dS0));
+  SEED_TRY(check_ws(ws, ws_bytes));
+  if (ws_bytes < seed::scan_workspace_bytes(*dims, true)) return SEED_ERR_WORKSPACE;
+  return seed::launch_scan_backward(*dims, offsets, q, k, v, alpha, beta, d_o, S0, dS_out, dq, dk, dv, dlog_alpha,
+                                    dbeta, dS0, ws, as_stream(stream));
+}
+
+int seed_decode_tree(const seed_dims* dims, const seed_state* state, int32_t layer, int32_t n_nodes,
+                     const int32_t* parent, const float* q, const float* k, const float* v, const float* alpha,
+                     const float* beta, float* o, float* w, void* ws, size_t ws_bytes, void* stream) {
+  SEED_TRY(check_tree(dims, layer, n_nodes));
+  SEED_TRY(check_state(state));
+  SEED_TRY(check_ptr(parent));
+  SEED_TRY(check_ptr(q));
+  SEED_TRY(check_ptr(k));
+  SEED_TRY(check_ptr(v));
+  SEED_TRY(check_ptr(alpha));
+  SEED_TRY(check_ptr(beta));
+  SEED_TRY(check_ptr(o));
+  SEED_TRY(check_ptr(w));
+  SEED_TRY(check_ws(ws, ws_bytes));
+  return seed::launch_decode_tree(*dims, *state, layer, n_nodes, parent, q, k, v, alpha, beta, o, w, status_word(ws),
+                                  as_stream(stream));
+}
+
+int seed_decode_tree_commit(const seed_dims* dims, const seed_state* state, int32_t layer, int32_t n_nodes,
+                            const int32_t* parent, const int32_t* leaf, const float* k, const float* v,
+                            const float* alpha, const float* beta, const float* w, void* ws, size_t ws_bytes,
+                            void* stream) {
+  SEED_TRY(check_tree(dims, layer, n_nodes));
+  SEED_TRY(check_state(state));
+  SEED_TRY(check_ptr(parent));
+  SEED_TRY(check_ptr(leaf));
+  SEED_TRY(check_ptr(k));
+  SEED_TRY(check_ptr(v));
+  SEED_TRY(check_ptr(alpha));
+  SEED_TRY(check_ptr(beta));
+  SEED_TRY(check_ptr(w));
+  SEED_TRY(check_ws(ws, ws_bytes));
+  return seed::launch_tree_commit(*dims, *state, layer, n_nodes, parent, leaf, k, v, alpha, beta, w, status_word(ws),
+                                  as_stream(stream));
 }
 
 int seed_get_status(void* ws, void* stream, uint32_t* flags) {

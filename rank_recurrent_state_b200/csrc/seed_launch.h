@@ -120,6 +120,25 @@ int launch_dense_step(const seed_dims& d, float* S, int layer, const float* q, c
                       const float* v, const float* alpha, const float* beta, float* o,
                       uint32_t* status, cudaStream_t st);
 
+size_t scan_workspace_bytes(const seed_scan_dims& d, bool backward);
+
+int launch_scan(const seed_scan_dims& d, const int32_t* offsets, const void* q, const void* k, const void* v,
+                const float* alpha, const float* beta, const float* S0, void* o, float* S_out, void* ws,
+                cudaStream_t st);
+
+int launch_scan_backward(const seed_scan_dims& d, const int32_t* offsets, const void* q, const void* k, const void* v,
+                         const float* alpha, const float* beta, const void* d_o, const float* S0, const float* dS_out,
+                         void* dq, void* dk, void* dv, float* dlog_alpha, float* dbeta, float* dS0, void* ws,
+                         cudaStream_t st);
+
+int launch_decode_tree(const seed_dims& d, const seed_state& s, int layer, int n_nodes, const int32_t* parent,
+                       const float* q, const float* k, const float* v, const float* alpha, const float* beta, float* o,
+                       float* w, uint32_t* status, cudaStream_t st);
+
+int launch_tree_commit(const seed_dims& d, const seed_state& s, int layer, int n_nodes, const int32_t* parent,
+                       const int32_t* leaf, const float* k, const float* v, const float* alpha, const float* beta,
+                       const float* w, uint32_t* status, cudaStream_t st);
+
 int launch_synth_vbar(const seed_dims& d, const seed_synth_key& key, float* vbar, cudaStream_t st);
 
 int launch_synth_token_inputs(const seed_dims& d, const seed_synth_key& key, int phase, int t,

@@ -1,0 +1,106 @@
+// seed_scan.cu -- the dense scan and its backward pass: scratch layout and the order
+// of the launches.  The scratch lies in the caller's workspace behind the status
+// words and is written anew by every call.
+#include "seed_scan.cuh"
+
+namespace seed {
+
+namespace {
+
+constexpr size_t kScratch0 = 256;      // the status words come first
+
+struct Carver {
+  size_t at = kScratch0;
+  unsigned char* base;
+  template <typename T>
+  T* take(long long n) {
+    T* p = base ? reinterpret_cast<T*>(base + at) : nullptr;
+    at += ((size_t)n * sizeof(T) + 255) & ~(size_t)255;
+    return p;
+  }
+};
+
+// Assigns the scratch pointers (null base: only counts) and returns the bytes used.
+size_t carve(ScanParams& p, bool backward, void* ws) {
+  Carver c;
+  c.base = static_cast<unsigned char*>(ws);
+  if (backward) {
+    const long long rows = p.tokens * p.H, mats = (long long)p.slots * p.H * p.dk * p.dv;
+    p.w = c.take<float>(rows * p.dv);
+    p.dw = c.take<float>(rows * p.dv);
+    p.chunk_S = c.take<float>(mats);
+    p.chunk_dS = c.take<float>(mats);
+    if (p.H != p.HK) p.part = c.take<float>(2 * rows * p.dk);
+  }
+  return c.at;
+}
+
+ScanParams params_of(const seed_scan_dims& d) {
+  ScanParams p{};
+  p.tokens = d.tokens;
+  p.seqs = d.seqs;
+  p.H = d.heads;
+  p.HK = d.k_heads;
+  p.dk = d.d_k;
+  p.dv = d.d_v;
+  p.elem = d.elem;
+  p.slots = (int)(d.tokens / kChunk) + d.seqs;
+  return p;
+}
+
+}  // namespace
+
+size_t scan_workspace_bytes(const seed_scan_dims& d, bool backward) {
+  ScanParams p = params_of(d);
+  return carve(p, backward, nullptr);
+}
+
+int launch_scan(const seed_scan_dims& d, const int32_t* offsets, const void* q, const void* k, const void* v,
+                const float* alpha, const float* beta, const float* S0, void* o, float* S_out, void* ws,
+                cudaStream_t st) {
+  ScanParams p = params_of(d);
+  carve(p, false, ws);
+  p.offsets = offsets;
+  p.q = q;
+  p.k = k;
+  p.v = v;
+  p.alpha = alpha;
+  p.beta = beta;
+  p.S0 = S0;
+  p.o = o;
+  p.S_out = S_out;
+  p.status = static_cast<uint32_t*>(ws);
+  return launch_scan_step(p, d.form, st);
+}
+
+int launch_scan_backward(const seed_scan_dims& d, const int32_t* offsets, const void* q, const void* k, const void* v,
+                         const float* alpha, const float* beta, const void* d_o, const float* S0, const float* dS_out,
+                         void* dq, void* dk, void* dv, float* dlog_alpha, float* dbeta, float* dS0, void* ws,
+                         cudaStream_t st) {
+  ScanParams p = params_of(d);
+  carve(p, true, ws);
+  p.offsets = offsets;
+  p.q = q;
+  p.k = k;
+  p.v = v;
+  p.alpha = alpha;
+  p.beta = beta;
+  p.S0 = S0;
+  p.d_o = d_o;
+  p.dS_out = dS_out;
+  p.dq = dq;
+  p.dk_ = dk;
+  p.dv_ = dv;
+  p.dlog_alpha = dlog_alpha;
+  p.dbeta = dbeta;
+  p.dS0 = dS0;
+  p.status = static_cast<uint32_t*>(ws);
+  int rc;
+  if ((rc = launch_scan_step(p, d.form, st))) return rc;          // w and the state before each chunk
+  if ((rc = launch_scan_step_back(p, d.form, st))) return rc;     // dw, the gradient behind each chunk, dS0
+  if (d.tokens == 0) return SEED_OK;
+  if ((rc = launch_scan_grad(p, d.form, st))) return rc;
+  return p.part ? launch_scan_share(p, st) : SEED_OK;
+}
+
+}  // namespace seed

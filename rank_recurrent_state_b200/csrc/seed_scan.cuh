@@ -1,0 +1,132 @@
+// seed_scan.cuh -- what the kernels of the dense scan (seed_dense_scan and its
+// backward pass) share: launch parameters, the chunk slots of packed ragged
+// sequences, and loads and stores of the three activation types.
+//
+// Notation, per head and per sequence (seed.h): a = decay, S' = Diag(a) S,
+// w = beta (v - S'^T k) (Mamba-2: beta v), S+ = S' + k w^T, o = S+^T q.  Inside a
+// chunk of kChunk tokens that starts from state S0, with B_i the product of the
+// decays up to token i and D_ij = B_i / B_j (formed as a product, never a quotient):
+//     S_i = B_i S0 + sum_{j <= i} D_ij k_j w_j^T
+#pragma once
+
+#include "seed_common.cuh"
+
+namespace seed {
+
+constexpr int kChunk = 64;
+
+struct ScanParams {
+  const int32_t* offsets;
+  const void* q;
+  const void* k;
+  const void* v;
+  const float* alpha;
+  const float* beta;
+  const float* S0;        // [seqs][H][dk][dv] or null (zeros)
+  void* o;                // null: not written
+  float* S_out;           // or null
+  // backward
+  const void* d_o;
+  const float* dS_out;    // or null (zeros)
+  void* dq;
+  void* dk_;
+  void* dv_;
+  float* dlog_alpha;
+  float* dbeta;
+  float* dS0;             // or null
+  // scratch (null where the call does not need them)
+  float* w;               // [tokens][H][dv]: the written values
+  float* dw;              // [tokens][H][dv]: their gradients
+  float* chunk_S;         // [slots][H][dk][dv]: the state before each chunk
+  float* chunk_dS;        // [slots][H][dk][dv]: the gradient of the state behind each chunk
+  float* part;            // [2][tokens][H][dk]: dq and dk per value head where heads share keys
+  uint32_t* status;
+  long long tokens;
+  int seqs, H, HK, dk, dv, elem, slots;
+};
+
+// ------------------------------------------------------------------ activations
+// elem is a seed_factors value; arithmetic is float32, stores round to nearest even.
+SEED_DEV float4 act_ld4(const void* p, long long i, int elem) {
+  if (elem == SEED_FACTORS_F32) return *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
+  if (elem == SEED_FACTORS_F16) return fac_ld4(static_cast<const __half*>(p) + i);
+  return fac_ld4(static_cast<const __nv_bfloat16*>(p) + i);
+}
+SEED_DEV float act_ld(const void* p, long long i, int elem) {
+  if (elem == SEED_FACTORS_F32) return static_cast<const float*>(p)[i];
+  if (elem == SEED_FACTORS_F16) return fac_to_f(static_cast<const __half*>(p)[i]);
+  return fac_to_f(static_cast<const __nv_bfloat16*>(p)[i]);
+}
+SEED_DEV void act_st4(void* p, long long i, float4 x, int elem) {
+  const float e[4] = {x.x, x.y, x.z, x.w};
+  if (elem == SEED_FACTORS_F32) fac_st<float, 4>(static_cast<float*>(p) + i, e);
+  else if (elem == SEED_FACTORS_F16) fac_st<__half, 4>(static_cast<__half*>(p) + i, e);
+  else fac_st<__nv_bfloat16, 4>(static_cast<__nv_bfloat16*>(p) + i, e);
+}
+SEED_DEV void act_st(void* p, long long i, float x, int elem) {
+  if (elem == SEED_FACTORS_F32) static_cast<float*>(p)[i] = x;
+  else if (elem == SEED_FACTORS_F16) static_cast<__half*>(p)[i] = __float2half_rn(x);
+  else static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(x);
+}
+// Whether x, once stored as elem, is finite.
+SEED_DEV bool act_finite(float x, int elem) {
+  return isfinite(elem == SEED_FACTORS_F16 ? fac_round<__half>(x)
+                                           : elem == SEED_FACTORS_BF16 ? fac_round<__nv_bfloat16>(x) : x);
+}
+
+// ------------------------------------------------------------------ packed sequences
+// Sequence s holds the rows offsets[s] .. offsets[s+1] of the packed arrays.  An
+// entry outside [0, tokens], or behind its successor, makes the sequence empty
+// (SEED_FLAG_BADINDEX): no row outside the arrays is ever touched.
+struct SeqRange {
+  long long first;
+  int len;
+  int slot0;     // first chunk slot
+};
+SEED_DEV SeqRange seq_range(const ScanParams& p, int s, bool raise) {
+  const long long a = p.offsets[s], b = p.offsets[s + 1];
+  if (a < 0 || b < a || b > p.tokens) {
+    if (raise) raise_flag(p.status, SEED_FLAG_BADINDEX);
+    return {0, 0, 0};
+  }
+  return {a, (int)(b - a), (int)(a / kChunk) + s};
+}
+
+// Chunk slots: chunk i of sequence s is slot offsets[s] / kChunk + s + i.  The slots
+// of different sequences never meet (floor(b/C) - floor(a/C) + 1 >= ceil((b-a)/C)),
+// all lie below tokens / kChunk + seqs, and the host needs no sequence length.
+// Returns false for a slot that holds no chunk.
+struct ChunkAt {
+  int seq, index, n;      // n: tokens of the chunk
+  long long first;        // its first row
+  bool last;              // the sequence's last chunk
+};
+SEED_DEV bool chunk_at(const ScanParams& p, int slot, ChunkAt* c) {
+  int lo = 0, hi = p.seqs - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    const int off = p.offsets[mid];
+    if ((off < 0 ? 0 : off / kChunk) + mid <= slot) lo = mid;
+    else hi = mid - 1;
+  }
+  const SeqRange r = seq_range(p, lo, false);
+  const int i = slot - r.slot0;
+  if (i < 0 || (long long)i * kChunk >= r.len) return false;
+  c->seq = lo;
+  c->index = i;
+  c->n = min(kChunk, r.len - i * kChunk);
+  c->first = r.first + (long long)i * kChunk;
+  c->last = (i + 1) * (long long)kChunk >= r.len;
+  return true;
+}
+
+// ------------------------------------------------------------------ launchers
+// Token-by-token kernels (seed_scan_step.cu).
+int launch_scan_step(const ScanParams& p, int form, cudaStream_t st);
+int launch_scan_step_back(const ScanParams& p, int form, cudaStream_t st);
+// Gradients of each chunk from its states (seed_scan_grad.cu).
+int launch_scan_grad(const ScanParams& p, int form, cudaStream_t st);
+// Sum of dq and dk over the heads that share a key head.
+int launch_scan_share(const ScanParams& p, cudaStream_t st);
+
+}  // namespace seed

@@ -1,0 +1,429 @@
+// seed_scan_grad.cu -- the gradients of one chunk of the dense scan from its states.
+//
+// For a chunk with the state S0 before it, the gradient dS of the state behind it,
+// the written values w_i and their gradients dw_i (all from the two recurrences), and
+// X_ij = do_i . w_j (j <= i), Y_ij = dw_i . w_j (j < i; zero for Mamba-2):
+//     dq_i = B_i (S0 do_i) + sum_{j<=i} X_ij D_ij k_j
+//     h_i  = B_i (S0 dw_i) + sum_{j<i}  Y_ij D_ij k_j            (= S'_i dw_i)
+//     c_i  = D_Ci (dS w_i) + sum_{m>=i} X_mi D_mi q_m - sum_{m>i} beta_m Y_mi D_mi k_m
+//     dk_i = c_i - beta_i h_i
+//     dv_i = beta_i dw_i,   dbeta_i = v_i . dw_i - k_i . h_i
+// per channel (summed over the channels where a head has one decay)
+//     d log a_t = sum_{i>=t} (q_i dq_i - beta_i k_i h_i - k_i c_i)
+//                 + B_C (S0 dS^T)_cc + sum_i k_i D_Ci (dS w_i)
+// The last line is the derivative along log a: finite where a decay is zero.  Its terms
+// that no decay touches (X_ii, and the last token's share of the state behind it) cancel
+// within it; they are left out, so that what has no decay in it is exactly zero.
+//
+// One block per (chunk, head), all products in float32 FMA from shared memory; the
+// decays run as products along the chunk, so zeros and per-channel decays need no case
+// of their own.  Bound by FMA issue and shared-memory reads.
+#include "seed_scan.cuh"
+
+namespace seed {
+
+namespace {
+
+constexpr int kNT = 256;
+
+template <int DK, int DV>
+struct GradSmem {
+  static constexpr int PK = DK + 4, PV = DV + 4;     // padded pitches (float4 rows, spread banks)
+  static constexpr int CT = 16;                      // state columns per tile
+  static constexpr int PT = CT + 4;
+  static constexpr int PX = kChunk + 4;
+  float q[kChunk * PK], k[kChunk * PK];
+  union {
+    struct { float d_o[kChunk * PV], w[kChunk * PV], dw[kChunk * PV]; } in;
+    struct { float dq[kChunk * PK], h[kChunk * PK], c[kChunk * PK]; } out;
+  };
+  union {
+    struct { float S0[DK * PT], dS[DK * PT]; } t;
+    struct { float X[kChunk * PX], Y[kChunk * PX]; } xy;
+  };
+  float alpha[kChunk], beta[kChunk], kh[kChunk], xd[kChunk], val[8];
+  float E[kNT];
+  float red[8][kChunk][2];
+};
+
+// Sum over groups of G consecutive lanes (G = min(32, DK)); every lane gets it.
+template <int G>
+SEED_DEV float lanes_sum(float x) { return group_sum<G>(x); }
+
+template <int FORM, int DK, int DV>
+__global__ void __launch_bounds__(kNT, 1) scan_grad_kernel(const ScanParams p) {
+  constexpr bool KDA = FORM == SEED_KDA, M2 = FORM == SEED_MAMBA2;
+  using Sm = GradSmem<DK, DV>;
+  constexpr int PK = Sm::PK, PV = Sm::PV, PT = Sm::PT, PX = Sm::PX, CT = Sm::CT;
+  extern __shared__ __align__(16) unsigned char smem_raw[];
+  Sm& sm = *reinterpret_cast<Sm*>(smem_raw);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int slot = blockIdx.x / p.H, h = blockIdx.x - slot * p.H;
+  ChunkAt ck;
+  if (!chunk_at(p, slot, &ck)) return;
+  const int n = ck.n;
+  const int hk = h / (p.H / p.HK);
+  const long long mat = (long long)DK * DV;
+  const float* S0 = p.chunk_S + ((long long)slot * p.H + h) * mat;
+  const float* dS = p.chunk_dS + ((long long)slot * p.H + h) * mat;
+  const float* al = p.alpha;
+
+  // ---- inputs; rows behind the chunk's tokens are zero
+  for (int e = tid; e < kChunk * DK / 4; e += kNT) {
+    const int i = e / (DK / 4), c = 4 * (e % (DK / 4));
+    float4 a = zero4(), b = zero4();
+    if (i < n) {
+      const long long at = ((ck.first + i) * p.HK + hk) * DK + c;
+      a = act_ld4(p.q, at, p.elem);
+      b = act_ld4(p.k, at, p.elem);
+    }
+    st4(&sm.q[i * PK + c], a);
+    st4(&sm.k[i * PK + c], b);
+  }
+  for (int e = tid; e < kChunk * DV / 4; e += kNT) {
+    const int i = e / (DV / 4), c = 4 * (e % (DV / 4));
+    float4 a = zero4(), b = zero4(), d = zero4();
+    if (i < n) {
+      const long long at = ((ck.first + i) * p.H + h) * DV + c;
+      a = act_ld4(p.d_o, at, p.elem);
+      b = ld4(p.w + at);
+      d = ld4(p.dw + at);
+    }
+    st4(&sm.in.d_o[i * PV + c], a);
+    st4(&sm.in.w[i * PV + c], b);
+    st4(&sm.in.dw[i * PV + c], d);
+  }
+  if (tid < kChunk) {
+    sm.beta[tid] = tid < n ? p.beta[(ck.first + tid) * p.H + h] : 0.f;
+    if constexpr (!KDA) sm.alpha[tid] = tid < n ? al[(ck.first + tid) * p.H + h] : 1.f;
+  }
+  __syncthreads();
+
+  // ---- dv and v . dw, a warp per row
+  for (int i = warp; i < n; i += kNT / 32) {
+    const long long row = ((ck.first + i) * p.H + h) * DV;
+    float x = 0.f;
+    for (int c = lane; c < DV; c += 32) {
+      const float d = sm.in.dw[i * PV + c];
+      x = fmaf(act_ld(p.v, row + c, p.elem), d, x);
+      act_st(p.dv_, row + c, sm.beta[i] * d, p.elem);
+    }
+    x = group_sum<32>(x);
+    if (lane == 0) sm.kh[i] = x;
+  }
+
+  // ---- S0 do, S0 dw, dS w: thread tile of 4 rows x DK / 16 columns
+  constexpr int NC = DK / 16;
+  const int ty = tid >> 4, tx = tid & 15;
+  float aq[4][NC] = {}, ah[4][NC] = {}, ac[4][NC] = {};
+  float E = 0.f;         // thread c < DK: (S0 dS^T)_cc
+  for (int j0 = 0; j0 < DV; j0 += CT) {
+    __syncthreads();
+    for (int e = tid; e < DK * CT / 4; e += kNT) {
+      const int c = e / (CT / 4), jj = 4 * (e % (CT / 4));
+      st4(&sm.t.S0[c * PT + jj], ld4(S0 + (long long)c * DV + j0 + jj));
+      st4(&sm.t.dS[c * PT + jj], ld4(dS + (long long)c * DV + j0 + jj));
+    }
+    __syncthreads();
+    if (tid < DK) {
+#pragma unroll
+      for (int jj = 0; jj < CT; jj += 4) E += dot4(ld4(&sm.t.S0[tid * PT + jj]), ld4(&sm.t.dS[tid * PT + jj]));
+    }
+#pragma unroll
+    for (int jj = 0; jj < CT; jj += 4) {
+      float4 xo[4], xd[4], xw[4];
+#pragma unroll
+      for (int a = 0; a < 4; ++a) {
+        const int at = (ty + 16 * a) * PV + j0 + jj;
+        xo[a] = ld4(&sm.in.d_o[at]);
+        if constexpr (!M2) xd[a] = ld4(&sm.in.dw[at]);
+        xw[a] = ld4(&sm.in.w[at]);
+      }
+#pragma unroll
+      for (int b = 0; b < NC; ++b) {
+        const float4 s = ld4(&sm.t.S0[(tx + 16 * b) * PT + jj]);
+        const float4 g = ld4(&sm.t.dS[(tx + 16 * b) * PT + jj]);
+#pragma unroll
+        for (int a = 0; a < 4; ++a) {
+          aq[a][b] += dot4(xo[a], s);
+          if constexpr (!M2) ah[a][b] += dot4(xd[a], s);
+          ac[a][b] += dot4(xw[a], g);
+        }
+      }
+    }
+  }
+  __syncthreads();
+  // ---- X and Y, kept as [column j][row i] (a row block of four is one float4)
+  {
+    float X[4][4] = {}, Y[4][4] = {};
+    for (int jj = 0; jj < DV; jj += 4) {
+      float4 xo[4], xd[4];
+#pragma unroll
+      for (int a = 0; a < 4; ++a) {
+        xo[a] = ld4(&sm.in.d_o[(ty + 16 * a) * PV + jj]);
+        if constexpr (!M2) xd[a] = ld4(&sm.in.dw[(ty + 16 * a) * PV + jj]);
+      }
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        const float4 w = ld4(&sm.in.w[(tx + 16 * b) * PV + jj]);
+#pragma unroll
+        for (int a = 0; a < 4; ++a) {
+          X[a][b] += dot4(xo[a], w);
+          if constexpr (!M2) Y[a][b] += dot4(xd[a], w);
+        }
+      }
+    }
+    // (the state tiles X and Y overlay were last read before the barrier above)
+#pragma unroll
+    for (int a = 0; a < 4; ++a)
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        const int i = ty + 16 * a, j = tx + 16 * b;
+        sm.xy.X[j * PX + i] = j < i ? X[a][b] : 0.f;
+        if (i == j) sm.xd[i] = X[a][b];
+        if constexpr (!M2) sm.xy.Y[j * PX + i] = j < i ? Y[a][b] : 0.f;
+      }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int a = 0; a < 4; ++a)
+#pragma unroll
+    for (int b = 0; b < NC; ++b) {
+      const int at = (ty + 16 * a) * PK + tx + 16 * b;
+      sm.out.dq[at] = aq[a][b];
+      if constexpr (!M2) sm.out.h[at] = ah[a][b];
+      sm.out.c[at] = ac[a][b];
+    }
+  __syncthreads();
+
+  // ---- sums over the chunk: a thread owns channel c and every NG-th block of 4 rows
+  constexpr int NG = kNT / DK;
+  constexpr int LG = DK < 32 ? DK : 32;
+  const int c = tid % DK, grp = tid / DK;
+  const float* arow = KDA ? al + (ck.first * p.H + h) * DK + c : nullptr;
+  const long long astep = (long long)p.H * DK;
+  auto dec = [&](int i) -> float {     // decay of token i (1 behind the chunk's tokens)
+    if constexpr (KDA) return i < n ? arow[i * astep] : 1.f;
+    else return sm.alpha[i];
+  };
+  float Epart = 0.f;
+  for (int i0 = 4 * grp; i0 < kChunk; i0 += 4 * NG) {
+    // rows i0 .. i0+3 against columns j <= i0, then the few inside the block
+    float sq[4] = {}, sh[4] = {};
+    float f = 1.f;
+    for (int j = i0; j >= 0; --j) {
+      const float t = f * sm.k[j * PK + c];
+      const float4 x = ld4(&sm.xy.X[j * PX + i0]);
+      sq[0] = fmaf(x.x, t, sq[0]); sq[1] = fmaf(x.y, t, sq[1]);
+      sq[2] = fmaf(x.z, t, sq[2]); sq[3] = fmaf(x.w, t, sq[3]);
+      if constexpr (!M2) {
+        const float4 y = ld4(&sm.xy.Y[j * PX + i0]);
+        sh[0] = fmaf(y.x, t, sh[0]); sh[1] = fmaf(y.y, t, sh[1]);
+        sh[2] = fmaf(y.z, t, sh[2]); sh[3] = fmaf(y.w, t, sh[3]);
+      }
+      f *= dec(j);
+    }
+    // f = B_i0; S0's part joins here
+    const float d1 = dec(i0 + 1), d2 = dec(i0 + 2), d3 = dec(i0 + 3);
+    const float fr[4] = {1.f, d1, d1 * d2, d1 * d2 * d3};
+    float k4[4];
+#pragma unroll
+    for (int a = 0; a < 4; ++a) {
+      const int at = (i0 + a) * PK + c;
+      sq[a] = fr[a] * fmaf(f, sm.out.dq[at], sq[a]);
+      if constexpr (!M2) sh[a] = fr[a] * fmaf(f, sm.out.h[at], sh[a]);
+      k4[a] = sm.k[at];
+    }
+#pragma unroll
+    for (int b = 1; b < 4; ++b) {      // column i0 + b, rows i0 + b .. i0 + 3
+      float t = k4[b];
+#pragma unroll
+      for (int a = b; a < 4; ++a) {
+        if (a > b) t *= a == 2 ? d2 : d3;
+        sq[a] = fmaf(sm.xy.X[(i0 + b) * PX + i0 + a], t, sq[a]);
+        if constexpr (!M2) sh[a] = fmaf(sm.xy.Y[(i0 + b) * PX + i0 + a], t, sh[a]);
+      }
+    }
+    // columns i0 .. i0+3 against rows m >= i0+3, then the few inside the block
+    float sc[4] = {};
+    f = 1.f;
+    for (int m = i0 + 3; m < kChunk; ++m) {
+      const float tq = f * sm.q[m * PK + c];
+      const float tk = M2 ? 0.f : -f * sm.beta[m] * sm.k[m * PK + c];
+#pragma unroll
+      for (int a = 0; a < 4; ++a) {
+        sc[a] = fmaf(sm.xy.X[(i0 + a) * PX + m], tq, sc[a]);
+        if constexpr (!M2) sc[a] = fmaf(sm.xy.Y[(i0 + a) * PX + m], tk, sc[a]);
+      }
+      if (m + 1 < kChunk) f *= dec(m + 1);
+    }
+    const float br[4] = {d1 * d2 * d3, d2 * d3, d3, 1.f};     // D between column i0 + a and row i0 + 3
+    float vs[4], kh[4], last[4];
+#pragma unroll
+    for (int a = 0; a < 4; ++a) {
+      const int at = (i0 + a) * PK + c;
+      const float end = br[a] * f * sm.out.c[at];              // D_Ci (dS w_i)
+      const bool crosses = i0 + a < n - 1;
+      if (crosses) Epart = fmaf(k4[a], end, Epart);
+      sc[a] = fmaf(br[a], sc[a], crosses ? end : 0.f);
+      last[a] = crosses ? 0.f : end;
+    }
+#pragma unroll
+    for (int b = 0; b < 3; ++b) {      // row i0 + b, columns i0 .. i0 + b
+      float tq = sm.q[(i0 + b) * PK + c];
+      float tk = M2 ? 0.f : -sm.beta[i0 + b] * k4[b];
+#pragma unroll
+      for (int a = b; a >= 0; --a) {
+        if (a < b) {
+          const float d = a == 0 ? d1 : d2;
+          tq *= d;
+          tk *= d;
+        }
+        sc[a] = fmaf(sm.xy.X[(i0 + a) * PX + i0 + b], tq, sc[a]);
+        if constexpr (!M2) sc[a] = fmaf(sm.xy.Y[(i0 + a) * PX + i0 + b], tk, sc[a]);
+      }
+    }
+#pragma unroll
+    for (int a = 0; a < 4; ++a) {
+      const int i = i0 + a;
+      const float be = sm.beta[i];
+      const float qi = sm.q[i * PK + c];
+      const float ci = fmaf(sm.xd[i], qi, sc[a]) + last[a];
+      const float dk = M2 ? ci : fmaf(-be, sh[a], ci);
+      const float dq = fmaf(sm.xd[i], k4[a], sq[a]);
+      kh[a] = M2 ? 0.f : k4[a] * sh[a];
+      vs[a] = qi * sq[a] - be * kh[a] - k4[a] * sc[a];
+      if (i < n) {
+        if (p.part != nullptr) {
+          const long long at = ((ck.first + i) * p.H + h) * DK + c;
+          p.part[at] = dq;
+          p.part[p.tokens * p.H * DK + at] = dk;
+        } else {
+          const long long at = ((ck.first + i) * p.HK + hk) * DK + c;
+          act_st(p.dq, at, dq, p.elem);
+          act_st(p.dk_, at, dk, p.elem);
+        }
+      }
+      if constexpr (!M2) kh[a] = lanes_sum<LG>(kh[a]);
+      if constexpr (KDA) sm.out.dq[i * PK + c] = vs[a];      // this thread alone reads and writes that element
+      else vs[a] = lanes_sum<LG>(vs[a]);
+      if ((c & (LG - 1)) == 0) {
+        sm.red[c / LG][i][0] = kh[a];
+        sm.red[c / LG][i][1] = vs[a];
+      }
+    }
+  }
+  sm.E[tid] = Epart;
+  __syncthreads();
+  // ---- dbeta, and the suffix sums of the decays' gradients
+  constexpr int NR = DK / LG;
+  if (tid < kChunk && tid < n) {
+    float x = 0.f;
+    if constexpr (!M2) {
+#pragma unroll
+      for (int r = 0; r < NR; ++r) x += sm.red[r][tid][0];
+    }
+    p.dbeta[(ck.first + tid) * p.H + h] = sm.kh[tid] - x;
+  }
+  if (tid < (DK < 32 ? 32 : DK)) {     // whole warps: the sums below are warp-wide
+    float e = 0.f;
+    if (tid < DK) {
+      float BC = 1.f;
+      for (int i = 0; i < n; ++i) BC *= dec(i);
+      e = BC * E;
+#pragma unroll
+      for (int g = 0; g < NG; ++g) e += sm.E[g * DK + tid];
+    }
+    if constexpr (KDA) {
+      if (tid < DK) {
+        for (int i = n - 1; i >= 0; --i) {
+          e += sm.out.dq[i * PK + tid];
+          p.dlog_alpha[((ck.first + i) * p.H + h) * DK + tid] = dec(i) == 0.f ? 0.f : e;
+        }
+      }
+    } else {
+      e = lanes_sum<LG>(e);
+      if (tid < DK && (tid & (LG - 1)) == 0) sm.val[tid / LG] = e;
+    }
+  }
+  if constexpr (!KDA) {
+    __syncthreads();
+    if (tid < 32) {
+      // suffix sums of 64 row values, two per lane
+      float e = 0.f;
+#pragma unroll
+      for (int r = 0; r < NR; ++r) e += sm.val[r];
+      float hi = 0.f, lo = 0.f;
+#pragma unroll
+      for (int r = 0; r < NR; ++r) {
+        lo += sm.red[r][2 * lane][1];
+        hi += sm.red[r][2 * lane + 1][1];
+      }
+      float tot = lo + hi;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const float x = __shfl_down_sync(0xffffffffu, tot, off);
+        if (lane + off < 32) tot += x;
+      }
+      // an inclusive sum of pairs: the odd token leaves its even neighbour's value out
+      float next = __shfl_down_sync(0xffffffffu, tot, 1);
+      if (lane == 31) next = 0.f;
+      if (2 * lane < n) p.dlog_alpha[(ck.first + 2 * lane) * p.H + h] = sm.alpha[2 * lane] == 0.f ? 0.f : e + tot;
+      if (2 * lane + 1 < n)
+        p.dlog_alpha[(ck.first + 2 * lane + 1) * p.H + h] = sm.alpha[2 * lane + 1] == 0.f ? 0.f : e + (hi + next);
+    }
+  }
+}
+
+__global__ void __launch_bounds__(256) scan_share_kernel(const ScanParams p) {
+  const long long per = p.tokens * p.HK * (p.dk / 4);
+  const int rep = p.H / p.HK;
+  for (long long e = blockIdx.x * 256ll + threadIdx.x; e < 2 * per; e += gridDim.x * 256ll) {
+    const int which = e >= per;
+    const long long x = e - which * per;
+    const int c = 4 * (int)(x % (p.dk / 4));
+    const long long th = x / (p.dk / 4);                // token * HK + key head
+    const long long t = th / p.HK;
+    if (t < p.offsets[0] || t >= p.offsets[p.seqs]) continue;
+    const float* src = p.part + which * p.tokens * p.H * p.dk + th * rep * p.dk + c;
+    float4 s = zero4();
+    for (int r = 0; r < rep; ++r) s = fma4(1.f, ld4(src + (long long)r * p.dk), s);
+    act_st4(which ? p.dk_ : p.dq, th * p.dk + c, s, p.elem);
+  }
+}
+
+template <int FORM, int DK, int DV>
+int launch_grad_t(const ScanParams& p, cudaStream_t st) {
+  static LaunchCache cache;
+  constexpr size_t bytes = sizeof(GradSmem<DK, DV>);
+  int dev;
+  if (int rc = cache.prepare(reinterpret_cast<const void*>(scan_grad_kernel<FORM, DK, DV>), bytes, &dev)) return rc;
+  const long long blocks = (long long)p.slots * p.H;
+  if (blocks > 0x7fffffffLL) return SEED_ERR_SHAPE;
+  scan_grad_kernel<FORM, DK, DV><<<(unsigned)blocks, kNT, bytes, st>>>(p);
+  return cudaGetLastError() == cudaSuccess ? SEED_OK : SEED_ERR_CUDA;
+}
+
+}  // namespace
+
+int launch_scan_grad(const ScanParams& p, int form, cudaStream_t st) {
+#define SEED_GRAD(F, K, V) \
+  if (form == F && p.dk == K && p.dv == V) return launch_grad_t<F, K, V>(p, st);
+#define SEED_GRAD_D(F) \
+  SEED_GRAD(F, 16, 16) SEED_GRAD(F, 32, 32) SEED_GRAD(F, 64, 64) SEED_GRAD(F, 128, 128) SEED_GRAD(F, 128, 64) SEED_GRAD(F, 64, 128)
+  SEED_GRAD_D(SEED_GDN)
+  SEED_GRAD_D(SEED_KDA)
+  SEED_GRAD_D(SEED_MAMBA2)
+#undef SEED_GRAD_D
+#undef SEED_GRAD
+  return SEED_ERR_SHAPE;
+}
+
+int launch_scan_share(const ScanParams& p, cudaStream_t st) {
+  const long long n = 2 * p.tokens * p.HK * (p.dk / 4);
+  const long long blocks = (n + 255) / 256;
+  scan_share_kernel<<<(unsigned)(blocks < 148 * 16 ? (blocks < 1 ? 1 : blocks) : 148 * 16), 256, 0, st>>>(p);
+  return cudaGetLastError() == cudaSuccess ? SEED_OK : SEED_ERR_CUDA;
+}
+
+}  // namespace seed

@@ -1,0 +1,443 @@
+// seed_tree.cu -- a tree of drafted tokens read against the stored state, and the
+// commit of its accepted path.
+//
+// Node t of a request's tree continues its parent's state, the roots the stored one,
+// S = a vbar^T + U V^T.  With B_t the product of the decays on the path to t and D_tj
+// that behind its ancestor j, every node's state is
+//     S_t = B_t S + sum_{j on the path to t, t included} D_tj k_j w_j^T
+//     w_t = beta_t (v_t - read(B_t k_t) - sum_{ancestors j} (k_t . D_tj k_j) w_j)
+//     o_t = read(B_t q_t) + sum_{j on the path, t included} (q_t . D_tj k_j) w_j
+//     read(x) = S^T x = vbar (a . x) + V (U^T x)
+// (Mamba-2: w_t = beta_t v_t).  So the stored columns are read once for all nodes,
+// and no node's d_k x d_v state is ever formed.
+//
+// One block per (request, head).  A warp walks a node's path to the root with the
+// running decay in registers (products, never quotients: a zero decay is an ordinary
+// value), which leaves k_t . D_tj k_j, q_t . D_tj k_j and the decayed k_t, q_t; the dot
+// products with the stored columns are a small product from shared memory; then each
+// thread owns a value channel and resolves the nodes in order.
+#include "seed_common.cuh"
+
+namespace seed {
+
+namespace {
+
+constexpr int kNT = 128;
+
+struct TreeParams {
+  const int32_t* parent;
+  const float* q;
+  const float* k;
+  const float* v;
+  const float* alpha;
+  const float* beta;
+  float* o;
+  float* w;
+  const float* a;
+  const void* U;
+  const void* V;
+  const float* scale;
+  const int32_t* ncols;
+  const float* vbar;
+  uint32_t* status;
+  int B, L, H, layer, m, slen, N, dk, dv;
+};
+
+// Shared-memory layout (floats).
+struct TreeSmem {
+  int rows, xs, us, ys, kk, pp, total;      // offsets; rows = 2 N rounded up to a multiple of 16
+  __host__ __device__ TreeSmem(int N, int m, int dk, int dv) {
+    rows = (2 * N + 15) & ~15;
+    xs = 0;
+    us = xs + rows * (dk + 4);
+    const int u1 = ((m + 1 + 3) & ~3) * (dk + 4), w1 = N * dv;
+    ys = us + (u1 > w1 ? u1 : w1);
+    kk = ys + (m + 1) * rows;
+    pp = kk + N * N;
+    total = pp + N * N;
+  }
+};
+
+template <int FORM, typename TS>
+__global__ void __launch_bounds__(kNT) decode_tree_kernel(const TreeParams p) {
+  constexpr bool KDA = FORM == SEED_KDA, M2 = FORM == SEED_MAMBA2;
+  extern __shared__ __align__(16) float smf[];
+  __shared__ int s_par[SEED_MAX_NODES];
+  __shared__ unsigned long long s_anc[SEED_MAX_NODES];     // ancestors, the node itself left out
+  const int N = p.N, dk = p.dk, dv = p.dv, PK = dk + 4;
+  const TreeSmem lay(N, p.m, dk, dv);
+  float* xs = smf + lay.xs;      // rows t: decayed k_t; rows rows/2 + t: decayed q_t
+  float* us = smf + lay.us;      // true U columns, then a; later w
+  float* ys = smf + lay.ys;      // [column][row]
+  float* kk = smf + lay.kk;
+  float* pp = smf + lay.pp;
+  const int half = lay.rows / 2;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int b = blockIdx.x / p.H, h = blockIdx.x - b * p.H;
+  const long long unit = ((long long)b * p.L + p.layer) * p.H + h;
+  const int c = p.ncols[unit];
+  if (c < 0 || c > p.m) {
+    if (tid == 0) raise_flag(p.status, SEED_FLAG_BADCOLS);
+    return;
+  }
+  const float* vb = p.vbar + ((long long)p.layer * p.H + h) * dv;
+
+  // ---- the tree: s_par[t] = parent, or -2 for an unused node.  A node is used when
+  // every step of its path goes to an earlier node and ends at -1.
+  if (tid < N) s_par[tid] = p.parent[(long long)b * N + tid];
+  __syncthreads();
+  int par = -2;
+  bool bad_tree = false;
+  if (tid < N) {
+    par = s_par[tid];
+    if (par >= -1) {
+      int u = tid;
+      while (u >= 0) {
+        const int up = s_par[u];
+        if (up < -1 || up >= u) {
+          bad_tree = true;
+          break;
+        }
+        u = up;
+      }
+      if (bad_tree) par = -2;
+    } else {
+      par = -2;
+    }
+  }
+  __syncthreads();
+  if (tid < N) s_par[tid] = par;
+  if (bad_tree && h == 0) raise_flag(p.status, SEED_FLAG_BADINDEX);
+  __syncthreads();
+
+  // ---- stored columns (true U) and a, beside them
+  const TS* U = static_cast<const TS*>(p.U) + unit * (long long)p.m * dk;
+  const float* sc = p.scale + unit * p.slen;
+  for (int e = tid; e < c * (dk / 4); e += kNT) {
+    const int j = e / (dk / 4), i = 4 * (e % (dk / 4));
+    float4 x = fac_ld4(U + (long long)j * dk + i);
+    if constexpr (KDA) x = mul4(x, ld4(sc + i));
+    else x = fma4(sc[j], x, zero4());
+    st4(us + j * PK + i, x);
+  }
+  for (int i = tid; i < dk; i += kNT) us[c * PK + i] = p.a[unit * dk + i];
+
+  // ---- paths
+  const long long row = (long long)b * N * p.H + h;     // token t: row + t H
+  for (int t = warp; t < half; t += kNT / 32) {
+    float kt[4], qt[4], f[4];
+    const bool used = t < N && s_par[t] >= -1;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int i = lane + 32 * e;
+      kt[e] = used && i < dk ? p.k[(row + (long long)t * p.H) * dk + i] : 0.f;
+      qt[e] = used && i < dk ? p.q[(row + (long long)t * p.H) * dk + i] : 0.f;
+      f[e] = 1.f;
+    }
+    unsigned long long anc = 0;
+    for (int j = used ? t : -1; j >= 0; j = s_par[j]) {
+      if (j != t) anc |= 1ull << j;
+      const long long rj = row + (long long)j * p.H;
+      float sk = 0.f, sq = 0.f;
+      const float g = KDA ? 1.f : p.alpha[rj];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int i = lane + 32 * e;
+        if (i < dk) {
+          const float kj = f[e] * p.k[rj * dk + i];
+          if constexpr (!M2) sk = fmaf(kt[e], kj, sk);
+          sq = fmaf(qt[e], kj, sq);
+          f[e] *= KDA ? p.alpha[rj * dk + i] : g;
+        }
+      }
+      sq = group_sum<32>(sq);
+      if constexpr (!M2) sk = group_sum<32>(sk);
+      if (lane == 0) {
+        pp[t * N + j] = sq;
+        if (!M2 && j != t) kk[t * N + j] = sk;
+      }
+    }
+    if (lane == 0 && t < N) s_anc[t] = anc;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int i = lane + 32 * e;
+      if (i < dk) {
+        xs[t * PK + i] = f[e] * kt[e];
+        xs[(half + t) * PK + i] = f[e] * qt[e];
+      }
+    }
+  }
+  __syncthreads();
+
+  // ---- ys[j][row] = x_row . (column j); column c is a.  Tiles of 4 rows x 2 columns.
+  const int ct = (c + 2) / 2;
+  for (int e = tid; e < (lay.rows / 4) * ct; e += kNT) {
+    const int r0 = 4 * (e % (lay.rows / 4)), j0 = 2 * (e / (lay.rows / 4));
+    const int j1 = j0 + 1 <= c ? j0 + 1 : j0;
+    float acc[4][2] = {};
+    if (!M2 || r0 + 3 >= half) {          // Mamba-2 reads the state with q alone
+      for (int i = 0; i < dk; i += 4) {
+        const float4 u0 = ld4(us + j0 * PK + i), u1 = ld4(us + j1 * PK + i);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const float4 x = ld4(xs + (r0 + r) * PK + i);
+          acc[r][0] += dot4(x, u0);
+          acc[r][1] += dot4(x, u1);
+        }
+      }
+    }
+    st4(ys + j0 * lay.rows + r0, make_float4(acc[0][0], acc[1][0], acc[2][0], acc[3][0]));
+    if (j1 != j0) st4(ys + j1 * lay.rows + r0, make_float4(acc[0][1], acc[1][1], acc[2][1], acc[3][1]));
+  }
+  __syncthreads();
+
+  // ---- value channels: a thread resolves its channel's w and o, nodes in order
+  float* ws = us;
+  bool bad = false;
+  for (int col = tid; col < dv; col += kNT) {
+    const TS* V = static_cast<const TS*>(p.V) + unit * (long long)p.m * dv + col;
+    const float vbc = vb[col];
+    for (int t0 = 0; t0 < N; t0 += 8) {
+      float rk[8], rq[8];
+#pragma unroll
+      for (int r = 0; r < 8; ++r) {
+        rk[r] = vbc * ys[c * lay.rows + t0 + r];
+        rq[r] = vbc * ys[c * lay.rows + half + t0 + r];
+      }
+      for (int j = 0; j < c; ++j) {
+        const float vj = fac_to_f(V[(long long)j * dv]);
+        const float* y = ys + j * lay.rows + t0;
+        if constexpr (!M2) {
+          const float4 a0 = ld4(y), a1 = ld4(y + 4);
+          rk[0] = fmaf(a0.x, vj, rk[0]); rk[1] = fmaf(a0.y, vj, rk[1]);
+          rk[2] = fmaf(a0.z, vj, rk[2]); rk[3] = fmaf(a0.w, vj, rk[3]);
+          rk[4] = fmaf(a1.x, vj, rk[4]); rk[5] = fmaf(a1.y, vj, rk[5]);
+          rk[6] = fmaf(a1.z, vj, rk[6]); rk[7] = fmaf(a1.w, vj, rk[7]);
+        }
+        const float4 b0 = ld4(y + half), b1 = ld4(y + half + 4);
+        rq[0] = fmaf(b0.x, vj, rq[0]); rq[1] = fmaf(b0.y, vj, rq[1]);
+        rq[2] = fmaf(b0.z, vj, rq[2]); rq[3] = fmaf(b0.w, vj, rq[3]);
+        rq[4] = fmaf(b1.x, vj, rq[4]); rq[5] = fmaf(b1.y, vj, rq[5]);
+        rq[6] = fmaf(b1.z, vj, rq[6]); rq[7] = fmaf(b1.w, vj, rq[7]);
+      }
+#pragma unroll
+      for (int r = 0; r < 8; ++r) {
+        const int t = t0 + r;
+        if (t < N) {
+          const long long rt = row + (long long)t * p.H;
+          const bool used = s_par[t] >= -1;
+          float w = 0.f, o = 0.f;
+          if (used) {
+            float x = p.v[rt * dv + col];
+            o = rq[r];
+            if constexpr (!M2) x -= rk[r];
+            // ancestors alone: another branch's values (NaN, say) never come in
+            for (unsigned long long anc = s_anc[t]; anc; anc &= anc - 1) {
+              const int j = __ffsll(anc) - 1;
+              const float wj = ws[j * dv + col];
+              if constexpr (!M2) x = fmaf(-kk[t * N + j], wj, x);
+              o = fmaf(pp[t * N + j], wj, o);
+            }
+            w = p.beta[rt] * x;
+            o = fmaf(pp[t * N + t], w, o);
+            bad = bad || !(isfinite(w) && isfinite(o));
+          }
+          ws[t * dv + col] = w;
+          p.w[rt * dv + col] = w;
+          p.o[rt * dv + col] = o;
+        }
+      }
+    }
+  }
+  if (bad) raise_flag(p.status, SEED_FLAG_NONFINITE);
+}
+
+// ------------------------------------------------------------------ commit
+// The accepted path's nodes as so many decode steps, without their read-outs: the sink
+// coefficient's own recurrence a+ = a' + s k with s = beta (omega - a' . k), a' = the
+// decayed a (Mamba-2: s = beta omega), the column pair (k, w - s vbar), the lazy scales.
+struct CommitParams {
+  const int32_t* parent;
+  const int32_t* leaf;
+  const float* k;
+  const float* v;
+  const float* alpha;
+  const float* beta;
+  const float* w;
+  float* a;
+  void* U;
+  void* V;
+  float* scale;
+  int32_t* ncols;
+  const float* vbar;
+  uint32_t* status;
+  int B, L, H, layer, m, slen, N, dk, dv;
+};
+
+template <int FORM, typename TS>
+__global__ void __launch_bounds__(kNT) tree_commit_kernel(const CommitParams p) {
+  constexpr bool KDA = FORM == SEED_KDA, M2 = FORM == SEED_MAMBA2;
+  __shared__ int s_path[SEED_MAX_NODES];
+  __shared__ float s_om[SEED_MAX_NODES], s_after[SEED_MAX_NODES + 1];
+  __shared__ float s_red[2][kNT / 32];
+  __shared__ int s_len;
+  const int N = p.N, dk = p.dk, dv = p.dv;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int b = blockIdx.x / p.H, h = blockIdx.x - b * p.H;
+  const long long unit = ((long long)b * p.L + p.layer) * p.H + h;
+  const int leaf = p.leaf[b];
+  if (leaf < 0) return;
+  const int c = p.ncols[unit];
+  if (tid == 0) {
+    int len = 0, u = leaf;
+    bool ok = leaf < N;
+    while (ok && u >= 0) {
+      const int up = p.parent[(long long)b * N + u];
+      if (up < -1 || up >= u) ok = false;
+      s_path[len++] = u;
+      u = up;
+    }
+    uint32_t flag = 0;
+    if (!ok) flag = SEED_FLAG_BADINDEX;
+    else if (c < 0 || c > p.m) flag = SEED_FLAG_BADCOLS;
+    else if (c + len > p.m) flag = SEED_FLAG_FULL;
+    if (flag) raise_flag(p.status, flag);
+    for (int i = 0; i < len / 2; ++i) {      // root first
+      const int x = s_path[i];
+      s_path[i] = s_path[len - 1 - i];
+      s_path[len - 1 - i] = x;
+    }
+    s_len = flag ? 0 : len;
+  }
+  __syncthreads();
+  const int len = s_len;
+  if (len == 0) return;
+  const long long row = (long long)b * N * p.H + h;
+  const float* vb = p.vbar + ((long long)p.layer * p.H + h) * dv;
+  float vv = 0.f;
+  for (int e = lane; e < dv; e += 32) vv = fmaf(vb[e], vb[e], vv);
+  vv = group_sum<32>(vv);
+  if (!(vv > 0.f)) {
+    if (tid == 0) raise_flag(p.status, SEED_FLAG_ZERO_VBAR);
+    return;
+  }
+  for (int i = warp; i < len; i += kNT / 32) {
+    const float* v = p.v + (row + (long long)s_path[i] * p.H) * dv;
+    float x = 0.f;
+    for (int e = lane; e < dv; e += 32) x = fmaf(v[e], vb[e], x);
+    x = group_sum<32>(x);
+    if (lane == 0) s_om[i] = x / vv;
+  }
+  if (!KDA && tid == 0) {
+    float f = 1.f;
+    for (int i = len - 1; i >= 0; --i) {      // s_after[i]: decay behind node i; [len] of the whole path
+      s_after[i] = f;
+      f *= p.alpha[row + (long long)s_path[i] * p.H];
+    }
+    s_after[len] = f;
+  }
+  __syncthreads();
+
+  bool bad = false;
+  const bool on = tid < dk;
+  float a = on ? p.a[unit * dk + tid] : 0.f;
+  float P = KDA && on ? p.scale[unit * dk + tid] : 1.f;
+  TS* U = static_cast<TS*>(p.U) + (unit * p.m + c) * (long long)dk;
+  TS* V = static_cast<TS*>(p.V) + (unit * p.m + c) * (long long)dv;
+  for (int i = 0; i < len; ++i) {
+    const long long rt = row + (long long)s_path[i] * p.H;
+    const float k = on ? p.k[rt * dk + tid] : 0.f;
+    const float al = KDA ? (on ? p.alpha[rt * dk + tid] : 1.f) : p.alpha[rt];
+    a *= al;
+    float ka = 0.f;
+    if constexpr (!M2) {
+      ka = group_sum<32>(k * a);
+      if (lane == 0) s_red[i & 1][warp] = ka;
+      __syncthreads();          // the other half is written only behind the next one
+      ka = 0.f;
+#pragma unroll
+      for (int x = 0; x < kNT / 32; ++x) ka += s_red[i & 1][x];
+    }
+    const float s = p.beta[rt] * (s_om[i] - ka);
+    a = fmaf(s, k, a);
+    if (on) {
+      float u = k;
+      if constexpr (KDA) {
+        P *= al;
+        u = k / P;
+      }
+      bad = bad || !isfinite(fac_round<TS>(u));
+      U[(long long)i * dk + tid] = fac_from_f<TS>(u);
+    }
+    for (int e = tid; e < dv; e += kNT) {
+      const float x = fmaf(-s, vb[e], p.w[rt * dv + e]);
+      bad = bad || !isfinite(fac_round<TS>(x));
+      V[(long long)i * dv + e] = fac_from_f<TS>(x);
+    }
+  }
+  if (on) {
+    p.a[unit * dk + tid] = a;
+    bad = bad || !isfinite(a);
+    if constexpr (KDA) p.scale[unit * dk + tid] = P;
+  }
+  if constexpr (!KDA) {
+    float* sc = p.scale + unit * p.slen;
+    for (int j = tid; j < c + len; j += kNT) sc[j] = j < c ? s_after[len] * sc[j] : s_after[j - c];
+  }
+  if (tid == 0) p.ncols[unit] = c + len;
+  if (bad) raise_flag(p.status, SEED_FLAG_NONFINITE);
+}
+
+template <int FORM, typename TS>
+int launch_tree_t(const TreeParams& p, cudaStream_t st) {
+  static LaunchCache cache;
+  const size_t bytes = sizeof(float) * (size_t)TreeSmem(p.N, p.m, p.dk, p.dv).total;
+  constexpr size_t most = 220 * 1024;      // 64 nodes, 96 columns, d 128: 199 KB
+  if (bytes > most) return SEED_ERR_SHAPE;
+  int dev;
+  if (int rc = cache.prepare(reinterpret_cast<const void*>(decode_tree_kernel<FORM, TS>), most, &dev)) return rc;
+  decode_tree_kernel<FORM, TS><<<p.B * p.H, kNT, bytes, st>>>(p);
+  return cudaGetLastError() == cudaSuccess ? SEED_OK : SEED_ERR_CUDA;
+}
+
+template <int FORM, typename TS>
+int launch_commit_t(const CommitParams& p, cudaStream_t st) {
+  tree_commit_kernel<FORM, TS><<<p.B * p.H, kNT, 0, st>>>(p);
+  return cudaGetLastError() == cudaSuccess ? SEED_OK : SEED_ERR_CUDA;
+}
+
+}  // namespace
+
+int launch_decode_tree(const seed_dims& d, const seed_state& s, int layer, int n_nodes, const int32_t* parent,
+                       const float* q, const float* k, const float* v, const float* alpha, const float* beta, float* o,
+                       float* w, uint32_t* status, cudaStream_t st) {
+  const TreeParams p{parent, q, k, v, alpha, beta, o, w, s.a, s.U, s.V, s.scale, s.ncols, s.vbar, status,
+                     d.batch, d.layers, d.heads, layer, d.R + d.W, scale_len(d), n_nodes, d.d_k, d.d_v};
+  return with_factor_type(d, [&](auto t) -> int {
+    using TS = decltype(t);
+    switch (d.form) {
+      case SEED_GDN: return launch_tree_t<SEED_GDN, TS>(p, st);
+      case SEED_KDA: return launch_tree_t<SEED_KDA, TS>(p, st);
+      case SEED_MAMBA2: return launch_tree_t<SEED_MAMBA2, TS>(p, st);
+    }
+    return SEED_ERR_INVALID_ARG;
+  });
+}
+
+int launch_tree_commit(const seed_dims& d, const seed_state& s, int layer, int n_nodes, const int32_t* parent,
+                       const int32_t* leaf, const float* k, const float* v, const float* alpha, const float* beta,
+                       const float* w, uint32_t* status, cudaStream_t st) {
+  const CommitParams p{parent, leaf, k, v, alpha, beta, w, s.a, s.U, s.V, s.scale, s.ncols, s.vbar, status,
+                       d.batch, d.layers, d.heads, layer, d.R + d.W, scale_len(d), n_nodes, d.d_k, d.d_v};
+  return with_factor_type(d, [&](auto t) -> int {
+    using TS = decltype(t);
+    switch (d.form) {
+      case SEED_GDN: return launch_commit_t<SEED_GDN, TS>(p, st);
+      case SEED_KDA: return launch_commit_t<SEED_KDA, TS>(p, st);
+      case SEED_MAMBA2: return launch_commit_t<SEED_MAMBA2, TS>(p, st);
+    }
+    return SEED_ERR_INVALID_ARG;
+  });
+}
+
+}  // namespace seed

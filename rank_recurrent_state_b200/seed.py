@@ -283,6 +283,142 @@ def seed_dense_step(dims: Dims, S: torch.Tensor, layer: int, q, k, v, alpha, bet
         ws.ptr, ws.nbytes, _stream(stream)))
 
 
+# ------------------------------------------------------------------ whole sequences
+
+SEED_MAX_NODES = 64
+
+
+@dataclass(frozen=True)
+class ScanDims:
+    """Packed sequences for seed_dense_scan and its backward pass (seed_scan_dims)."""
+    form: int
+    seqs: int
+    tokens: int
+    heads: int
+    k_heads: int
+    d_k: int
+    d_v: int
+    max_len: int
+    elem: int = SEED_FACTORS_F32     # element type of q, k, v, o
+
+    def c(self) -> _lib.seed_scan_dims:
+        return _lib.seed_scan_dims(self.form, self.seqs, self.heads, self.k_heads, self.d_k, self.d_v,
+                                   self.max_len, self.elem, self.tokens)
+
+    @property
+    def dtype(self) -> torch.dtype:
+        return FACTOR_DTYPES[self.elem]
+
+
+class ScanWorkspace:
+    """Status words and scratch for seed_dense_scan (backward=True: and its backward pass)."""
+
+    def __init__(self, dims: ScanDims, backward: bool = False, device="cuda"):
+        lib = _lib.load()
+        d = dims.c()
+        self.nbytes = int(lib.seed_scan_workspace_bytes(ctypes.byref(d), 1 if backward else 0))
+        if self.nbytes == 0:
+            raise ValueError(f"unsupported dims {dims}")
+        self.buf = torch.empty(self.nbytes, dtype=torch.uint8, device=device)
+        with torch.cuda.device(self.buf.device):
+            _check("seed_workspace_init", lib.seed_workspace_init(_ptr(self.buf), self.nbytes, _stream(None)))
+
+    @property
+    def ptr(self) -> int:
+        return self.buf.data_ptr()
+
+
+def _check_arrays(where: torch.device, **arrays) -> None:
+    """The C ABI sees only pointers: every array (name=(tensor, dtype, elements); None is
+    an absent optional one) has its element type, its size, and lies on `where`."""
+    for name, (t, dtype, n) in arrays.items():
+        if t is None:
+            continue
+        if t.dtype != dtype or t.numel() != n:
+            raise ValueError(f"{name}: expected {dtype} with {n} elements, got {t.dtype} with {t.numel()}")
+        if t.device != where:
+            raise ValueError(f"{name}: on {t.device}, the workspace on {where}")
+
+
+def _scan_arrays(d: ScanDims) -> dict:
+    qk, v, g = d.tokens * d.k_heads * d.d_k, d.tokens * d.heads * d.d_v, d.tokens * d.heads
+    f32 = torch.float32
+    return {"offsets": (torch.int32, d.seqs + 1), "qk": (d.dtype, qk), "v": (d.dtype, v),
+            "alpha": (f32, g * d.d_k if d.form == SEED_KDA else g), "beta": (f32, g),
+            "S": (f32, d.seqs * d.heads * d.d_k * d.d_v)}
+
+
+def seed_dense_scan(dims: ScanDims, offsets, q, k, v, alpha, beta, o, ws: ScanWorkspace,
+                    S0: torch.Tensor | None = None, S_out: torch.Tensor | None = None, stream=None) -> None:
+    """The dense recurrence over packed sequences; offsets int32 [seqs + 1] on the device."""
+    a = _scan_arrays(dims)
+    _check_arrays(ws.buf.device, offsets=(offsets, *a["offsets"]), q=(q, *a["qk"]), k=(k, *a["qk"]), v=(v, *a["v"]),
+                  alpha=(alpha, *a["alpha"]), beta=(beta, *a["beta"]), o=(o, *a["v"]), S0=(S0, *a["S"]),
+                  S_out=(S_out, *a["S"]))
+    d = dims.c()
+    with torch.cuda.device(ws.buf.device):
+        _check("seed_dense_scan", _lib.load().seed_dense_scan(
+            ctypes.byref(d), _ptr(offsets), _ptr(q), _ptr(k), _ptr(v), _ptr(alpha), _ptr(beta), _ptr(S0), _ptr(o),
+            _ptr(S_out), ws.ptr, ws.nbytes, _stream(stream)))
+
+
+def seed_dense_scan_backward(dims: ScanDims, offsets, q, k, v, alpha, beta, d_o, dq, dk, dv, dlog_alpha, dbeta,
+                             ws: ScanWorkspace, S0: torch.Tensor | None = None, dS_out: torch.Tensor | None = None,
+                             dS0: torch.Tensor | None = None, stream=None) -> None:
+    """Gradients of seed_dense_scan into dq, dk, dv, dlog_alpha, dbeta and dS0 (see seed.h)."""
+    a = _scan_arrays(dims)
+    _check_arrays(ws.buf.device, offsets=(offsets, *a["offsets"]), q=(q, *a["qk"]), k=(k, *a["qk"]), v=(v, *a["v"]),
+                  alpha=(alpha, *a["alpha"]), beta=(beta, *a["beta"]), d_o=(d_o, *a["v"]), dq=(dq, *a["qk"]),
+                  dk=(dk, *a["qk"]), dv=(dv, *a["v"]), dlog_alpha=(dlog_alpha, *a["alpha"]),
+                  dbeta=(dbeta, *a["beta"]), S0=(S0, *a["S"]), dS_out=(dS_out, *a["S"]), dS0=(dS0, *a["S"]))
+    d = dims.c()
+    with torch.cuda.device(ws.buf.device):
+        _check("seed_dense_scan_backward", _lib.load().seed_dense_scan_backward(
+            ctypes.byref(d), _ptr(offsets), _ptr(q), _ptr(k), _ptr(v), _ptr(alpha), _ptr(beta), _ptr(d_o), _ptr(S0),
+            _ptr(dS_out), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dlog_alpha), _ptr(dbeta), _ptr(dS0), ws.ptr, ws.nbytes,
+            _stream(stream)))
+
+
+# ------------------------------------------------------------------ drafted tokens
+
+def _tree_arrays(dims: Dims, parent: torch.Tensor) -> tuple:
+    if parent.dim() != 2 or parent.shape[0] != dims.batch:
+        raise ValueError(f"parent: expected [{dims.batch}][nodes], got {tuple(parent.shape)}")
+    n = int(parent.shape[1])
+    g = dims.batch * n * dims.heads
+    f32 = torch.float32
+    return n, {"parent": (torch.int32, dims.batch * n), "k": (f32, g * dims.d_k), "v": (f32, g * dims.d_v),
+               "alpha": (f32, g * dims.d_k if dims.form == SEED_KDA else g), "beta": (f32, g)}
+
+
+def seed_decode_tree(dims: Dims, state: State, layer: int, parent, q, k, v, alpha, beta, o, w, ws: Workspace,
+                     stream=None) -> None:
+    """Read a tree of drafted tokens against the stored state: parent [B][N] int32 (see seed.h)."""
+    _check_state(dims, state)
+    n, a = _tree_arrays(dims, parent)
+    _check_arrays(ws.buf.device, parent=(parent, *a["parent"]), q=(q, *a["k"]), k=(k, *a["k"]), v=(v, *a["v"]),
+                  alpha=(alpha, *a["alpha"]), beta=(beta, *a["beta"]), o=(o, *a["v"]), w=(w, *a["v"]))
+    d, s = dims.c(), state.c()
+    with torch.cuda.device(ws.buf.device):
+        _check("seed_decode_tree", _lib.load().seed_decode_tree(
+            ctypes.byref(d), ctypes.byref(s), layer, n, _ptr(parent), _ptr(q), _ptr(k), _ptr(v), _ptr(alpha),
+            _ptr(beta), _ptr(o), _ptr(w), ws.ptr, ws.nbytes, _stream(stream)))
+
+
+def seed_decode_tree_commit(dims: Dims, state: State, layer: int, parent, leaf, k, v, alpha, beta, w, ws: Workspace,
+                            stream=None) -> None:
+    """Append the path to node leaf[b] (int32 [B]; negative: none) to the stored state."""
+    _check_state(dims, state)
+    n, a = _tree_arrays(dims, parent)
+    _check_arrays(ws.buf.device, parent=(parent, *a["parent"]), leaf=(leaf, torch.int32, dims.batch), k=(k, *a["k"]),
+                  v=(v, *a["v"]), alpha=(alpha, *a["alpha"]), beta=(beta, *a["beta"]), w=(w, *a["v"]))
+    d, s = dims.c(), state.c()
+    with torch.cuda.device(ws.buf.device):
+        _check("seed_decode_tree_commit", _lib.load().seed_decode_tree_commit(
+            ctypes.byref(d), ctypes.byref(s), layer, n, _ptr(parent), _ptr(leaf), _ptr(k), _ptr(v), _ptr(alpha),
+            _ptr(beta), _ptr(w), ws.ptr, ws.nbytes, _stream(stream)))
+
+
 def seed_get_status(ws: Workspace, stream=None) -> int:
     flags = _lib.c_uint32(0)
     _check("seed_get_status", _lib.load().seed_get_status(ws.ptr, _stream(stream), ctypes.byref(flags)))
