@@ -20,10 +20,18 @@ struct Carver {
   }
 };
 
+// The chunked passes take d_k and d_v of 64 and 128 from kStepMost tokens on; shorter
+// sequences and smaller heads go token by token.
+constexpr int kStepMost = 32;
+bool chunked(const ScanParams& p, const seed_scan_dims& d) {
+  return p.dk >= 64 && p.dv >= 64 && d.max_len > kStepMost;
+}
+
 // Assigns the scratch pointers (null base: only counts) and returns the bytes used.
-size_t carve(ScanParams& p, bool backward, void* ws) {
+size_t carve(ScanParams& p, const seed_scan_dims& d, bool backward, void* ws) {
   Carver c;
   c.base = static_cast<unsigned char*>(ws);
+  if (chunked(p, d)) p.tri = c.take<unsigned char>((long long)p.slots * p.H * kTriBytes);
   if (backward) {
     const long long rows = p.tokens * p.H, mats = (long long)p.slots * p.H * p.dk * p.dv;
     p.w = c.take<float>(rows * p.dv);
@@ -33,6 +41,15 @@ size_t carve(ScanParams& p, bool backward, void* ws) {
     if (p.H != p.HK) p.part = c.take<float>(2 * rows * p.dk);
   }
   return c.at;
+}
+
+// Forward, or its recomputation: o, S_out, w and chunk_S where they are asked for.
+int forward(const ScanParams& p, const seed_scan_dims& d, cudaStream_t st) {
+  if (!chunked(p, d)) return launch_scan_step(p, d.form, st);
+  if (d.tokens > 0) {
+    if (const int rc = launch_scan_prep(p, d.form, st)) return rc;
+  }
+  return launch_scan_pass(p, d.form, st);
 }
 
 ScanParams params_of(const seed_scan_dims& d) {
@@ -52,14 +69,14 @@ ScanParams params_of(const seed_scan_dims& d) {
 
 size_t scan_workspace_bytes(const seed_scan_dims& d, bool backward) {
   ScanParams p = params_of(d);
-  return carve(p, backward, nullptr);
+  return carve(p, d, backward, nullptr);
 }
 
 int launch_scan(const seed_scan_dims& d, const int32_t* offsets, const void* q, const void* k, const void* v,
                 const float* alpha, const float* beta, const float* S0, void* o, float* S_out, void* ws,
                 cudaStream_t st) {
   ScanParams p = params_of(d);
-  carve(p, false, ws);
+  carve(p, d, false, ws);
   p.offsets = offsets;
   p.q = q;
   p.k = k;
@@ -70,7 +87,7 @@ int launch_scan(const seed_scan_dims& d, const int32_t* offsets, const void* q, 
   p.o = o;
   p.S_out = S_out;
   p.status = static_cast<uint32_t*>(ws);
-  return launch_scan_step(p, d.form, st);
+  return forward(p, d, st);
 }
 
 int launch_scan_backward(const seed_scan_dims& d, const int32_t* offsets, const void* q, const void* k, const void* v,
@@ -78,7 +95,7 @@ int launch_scan_backward(const seed_scan_dims& d, const int32_t* offsets, const 
                          void* dq, void* dk, void* dv, float* dlog_alpha, float* dbeta, float* dS0, void* ws,
                          cudaStream_t st) {
   ScanParams p = params_of(d);
-  carve(p, true, ws);
+  carve(p, d, true, ws);
   p.offsets = offsets;
   p.q = q;
   p.k = k;
@@ -96,7 +113,7 @@ int launch_scan_backward(const seed_scan_dims& d, const int32_t* offsets, const 
   p.dS0 = dS0;
   p.status = static_cast<uint32_t*>(ws);
   int rc;
-  if ((rc = launch_scan_step(p, d.form, st))) return rc;          // w and the state before each chunk
+  if ((rc = forward(p, d, st))) return rc;                        // w and the state before each chunk
   if ((rc = launch_scan_step_back(p, d.form, st))) return rc;     // dw, the gradient behind each chunk, dS0
   if (d.tokens == 0) return SEED_OK;
   if ((rc = launch_scan_grad(p, d.form, st))) return rc;

@@ -14,6 +14,9 @@
 namespace seed {
 
 constexpr int kChunk = 64;
+// Scratch of one chunk and head for the chunked passes: the images of T and P (two fp16
+// terms of 64 x 64 each) and their rows' scales.
+constexpr int kTriBytes = 4 * 8192 + 2 * kChunk * 4;
 
 struct ScanParams {
   const int32_t* offsets;
@@ -40,6 +43,7 @@ struct ScanParams {
   float* chunk_S;         // [slots][H][dk][dv]: the state before each chunk
   float* chunk_dS;        // [slots][H][dk][dv]: the gradient of the state behind each chunk
   float* part;            // [2][tokens][H][dk]: dq and dk per value head where heads share keys
+  unsigned char* tri;     // [slots][H][kTriBytes]
   uint32_t* status;
   long long tokens;
   int seqs, H, HK, dk, dv, elem, slots;
@@ -124,6 +128,10 @@ SEED_DEV bool chunk_at(const ScanParams& p, int slot, ChunkAt* c) {
 // Token-by-token kernels (seed_scan_step.cu).
 int launch_scan_step(const ScanParams& p, int form, cudaStream_t st);
 int launch_scan_step_back(const ScanParams& p, int form, cudaStream_t st);
+// T and P of every chunk (seed_scan_prep.cu), d_k in {64, 128}.
+int launch_scan_prep(const ScanParams& p, int form, cudaStream_t st);
+// The chunked passes on the tensor cores (seed_scan_pass.cu), d_k and d_v in {64, 128}.
+int launch_scan_pass(const ScanParams& p, int form, cudaStream_t st);
 // Gradients of each chunk from its states (seed_scan_grad.cu).
 int launch_scan_grad(const ScanParams& p, int form, cudaStream_t st);
 // Sum of dq and dk over the heads that share a key head.
