@@ -61,15 +61,20 @@ inline int scale_len(const seed_dims& d) {
 // Bytes of one element of U and V.
 inline int factor_bytes(const seed_dims& d) { return d.factors == SEED_FACTORS_F32 ? 4 : 2; }
 
-// f(T{}) with T the element type of U and V (float, __half or __nv_bfloat16).
+// f(T{}) with T the element type `factors` names (float, __half or __nv_bfloat16).
 template <typename F>
-int with_factor_type(const seed_dims& d, F&& f) {
-  switch (d.factors) {
+int with_factor_type_of(int32_t factors, F&& f) {
+  switch (factors) {
     case SEED_FACTORS_F32: return f(float{});
     case SEED_FACTORS_F16: return f(__half{});
     case SEED_FACTORS_BF16: return f(__nv_bfloat16{});
   }
   return SEED_ERR_INVALID_ARG;
+}
+// The same for the element type of U and V.
+template <typename F>
+int with_factor_type(const seed_dims& d, F&& f) {
+  return with_factor_type_of(d.factors, f);
 }
 
 bool decode_dims_supported(int dk, int dv);

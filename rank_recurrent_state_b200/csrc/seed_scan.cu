@@ -49,7 +49,7 @@ int forward(const ScanParams& p, const seed_scan_dims& d, cudaStream_t st) {
   if (d.tokens > 0) {
     if (const int rc = launch_scan_prep(p, d.form, st)) return rc;
   }
-  return launch_scan_pass(p, d.form, st);
+  return with_factor_type_of(d.elem, [&](auto t) -> int { return launch_scan_pass_as<decltype(t)>(p, d.form, st); });
 }
 
 ScanParams params_of(const seed_scan_dims& d) {

@@ -72,6 +72,70 @@ SEED_DEV void act_st(void* p, long long i, float x, int elem) {
   else if (elem == SEED_FACTORS_F16) static_cast<__half*>(p)[i] = __float2half_rn(x);
   else static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(x);
 }
+// f(T{}) with T the activation type: around loops of loads, which must not branch on
+// elem between one load and the next (each would wait for the one before).
+template <typename F>
+SEED_DEV void act_type(int elem, F&& f) {
+  if (elem == SEED_FACTORS_F32) f(float{});
+  else if (elem == SEED_FACTORS_F16) f(__half{});
+  else f(__nv_bfloat16{});
+}
+// N values `step` apart (zeros from the left-th on).  All loads are issued before the
+// first conversion: a conversion under the loads' predicate becomes a branch per value,
+// each waiting for its load (32 bf16 values of 48 heads: 20,000 cycles against 1,000).
+template <typename T, int N>
+SEED_DEV void act_ld_rows(const T* src, long long step, int left, float (&x)[N]) {
+  if constexpr (std::is_same<T, float>::value) {
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      x[e] = 0.f;
+      if (e < left) x[e] = src[e * step];
+    }
+  } else {
+    uint16_t raw[N];
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      raw[e] = 0;
+      if (e < left) raw[e] = reinterpret_cast<const uint16_t*>(src)[e * step];
+    }
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      T t;
+      memcpy(&t, &raw[e], 2);
+      x[e] = fac_to_f(t);
+    }
+  }
+}
+// The stores that go with it.
+template <typename T, int N>
+SEED_DEV void act_st_rows(T* dst, long long step, int left, const float (&x)[N]) {
+  T t[N];
+#pragma unroll
+  for (int e = 0; e < N; ++e) t[e] = fac_from_f<T>(x[e]);
+#pragma unroll
+  for (int e = 0; e < N; ++e)
+    if (e < left) dst[e * step] = t[e];
+}
+// N groups of eight consecutive values, `step` elements apart.
+template <typename T, int N>
+SEED_DEV void act_ld8_rows(const T* src, long long step, int left, float (&x)[N][8]) {
+  constexpr int Q = sizeof(T) / 2;      // 16-byte loads per group
+  uint4 raw[N][Q];
+#pragma unroll
+  for (int e = 0; e < N; ++e)
+#pragma unroll
+    for (int y = 0; y < Q; ++y) {
+      raw[e][y] = make_uint4(0, 0, 0, 0);
+      if (e < left) raw[e][y] = reinterpret_cast<const uint4*>(src + e * step)[y];
+    }
+#pragma unroll
+  for (int e = 0; e < N; ++e) {
+    T t[8];
+    memcpy(t, raw[e], sizeof(t));
+#pragma unroll
+    for (int y = 0; y < 8; ++y) x[e][y] = fac_to_f(t[y]);
+  }
+}
 // Whether x, once stored as elem, is finite.
 SEED_DEV bool act_finite(float x, int elem) {
   return isfinite(elem == SEED_FACTORS_F16 ? fac_round<__half>(x)
@@ -130,8 +194,10 @@ int launch_scan_step(const ScanParams& p, int form, cudaStream_t st);
 int launch_scan_step_back(const ScanParams& p, int form, cudaStream_t st);
 // T and P of every chunk (seed_scan_prep.cu), d_k in {64, 128}.
 int launch_scan_prep(const ScanParams& p, int form, cudaStream_t st);
-// The chunked passes on the tensor cores (seed_scan_pass.cu), d_k and d_v in {64, 128}.
-int launch_scan_pass(const ScanParams& p, int form, cudaStream_t st);
+// The chunked pass on the tensor cores for activations of type T (seed_scan_pass.cuh),
+// d_k and d_v in {64, 128}; writes w and chunk_S instead of o and S_out where chunk_S is set.
+template <typename T>
+int launch_scan_pass_as(const ScanParams& p, int form, cudaStream_t st);
 // Gradients of each chunk from its states (seed_scan_grad.cu).
 int launch_scan_grad(const ScanParams& p, int form, cudaStream_t st);
 // Sum of dq and dk over the heads that share a key head.

@@ -69,30 +69,35 @@ __global__ void __launch_bounds__(kNT, 1) scan_grad_kernel(const ScanParams p) {
   const float* al = p.alpha;
 
   // ---- inputs; rows behind the chunk's tokens are zero
-  for (int e = tid; e < kChunk * DK / 4; e += kNT) {
-    const int i = e / (DK / 4), c = 4 * (e % (DK / 4));
-    float4 a = zero4(), b = zero4();
-    if (i < n) {
-      const long long at = ((ck.first + i) * p.HK + hk) * DK + c;
-      a = act_ld4(p.q, at, p.elem);
-      b = act_ld4(p.k, at, p.elem);
+  act_type(p.elem, [&](auto tag) {
+    using E = decltype(tag);
+#pragma unroll 4
+    for (int e = tid; e < kChunk * DK / 4; e += kNT) {
+      const int i = e / (DK / 4), c = 4 * (e % (DK / 4));
+      float4 a = zero4(), b = zero4();
+      if (i < n) {
+        const long long at = ((ck.first + i) * p.HK + hk) * DK + c;
+        a = fac_ld4(static_cast<const E*>(p.q) + at);
+        b = fac_ld4(static_cast<const E*>(p.k) + at);
+      }
+      st4(&sm.q[i * PK + c], a);
+      st4(&sm.k[i * PK + c], b);
     }
-    st4(&sm.q[i * PK + c], a);
-    st4(&sm.k[i * PK + c], b);
-  }
-  for (int e = tid; e < kChunk * DV / 4; e += kNT) {
-    const int i = e / (DV / 4), c = 4 * (e % (DV / 4));
-    float4 a = zero4(), b = zero4(), d = zero4();
-    if (i < n) {
-      const long long at = ((ck.first + i) * p.H + h) * DV + c;
-      a = act_ld4(p.d_o, at, p.elem);
-      b = ld4(p.w + at);
-      d = ld4(p.dw + at);
+#pragma unroll 4
+    for (int e = tid; e < kChunk * DV / 4; e += kNT) {
+      const int i = e / (DV / 4), c = 4 * (e % (DV / 4));
+      float4 a = zero4(), b = zero4(), d = zero4();
+      if (i < n) {
+        const long long at = ((ck.first + i) * p.H + h) * DV + c;
+        a = fac_ld4(static_cast<const E*>(p.d_o) + at);
+        b = ld4(p.w + at);
+        d = ld4(p.dw + at);
+      }
+      st4(&sm.in.d_o[i * PV + c], a);
+      st4(&sm.in.w[i * PV + c], b);
+      st4(&sm.in.dw[i * PV + c], d);
     }
-    st4(&sm.in.d_o[i * PV + c], a);
-    st4(&sm.in.w[i * PV + c], b);
-    st4(&sm.in.dw[i * PV + c], d);
-  }
+  });
   if (tid < kChunk) {
     sm.beta[tid] = tid < n ? p.beta[(ck.first + tid) * p.H + h] : 0.f;
     if constexpr (!KDA) sm.alpha[tid] = tid < n ? al[(ck.first + tid) * p.H + h] : 1.f;

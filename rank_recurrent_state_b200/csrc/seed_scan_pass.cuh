@@ -1,4 +1,4 @@
-// seed_scan_pass.cu -- the dense scan chunk by chunk on the tensor cores.
+// seed_scan_pass.cuh -- the dense scan chunk by chunk on the tensor cores.
 //
 // One block per (sequence, head) walks its chunks of 64 tokens with S^T (value channel
 // x key channel) in registers.  Per chunk, with T and P from seed_scan_prep.cu, Kb and Qb
@@ -20,6 +20,8 @@
 //
 // Waits are bounded: one that runs out raises SEED_FLAG_TIMEOUT, and every later wait of
 // the block returns at once, so that it ends (with unspecified results).
+#pragma once
+
 #include "seed_scan.cuh"
 #include "seed_umma.cuh"
 
@@ -84,25 +86,24 @@ SEED_DEV void pass_wait(uint64_t* bar, uint32_t phase, volatile int* dead, uint3
 }
 
 // Three products (hi hi, hi lo, lo hi) of an A operand in tensor memory (lo terms
-// a_lo columns behind the hi ones) with a tile in shared memory (lo terms b_lo bytes
-// behind).  KS steps of 16; step(ks): byte offset of a step in the tile.
-template <int KS, typename Step>
-SEED_DEV void product(uint32_t d, uint32_t a, uint32_t a_lo, uint32_t tile, uint32_t b_lo, uint32_t lbo,
-                      uint32_t idesc, Step step) {
-  bool acc = false;
+// A_LO columns behind the hi ones) with a tile in shared memory (its descriptor; lo terms
+// B_LO bytes behind).  KS steps of 16; step(ks): byte offset of a step in the tile.
+template <int KS, uint32_t A_LO, uint32_t B_LO, uint32_t IDESC, typename Step>
+SEED_DEV void product(uint32_t d, uint32_t a, uint64_t tile, Step step) {
 #pragma unroll
   for (int t = 0; t < 3; ++t) {
-    const uint32_t at = t == 2 ? a + a_lo : a;
-    const uint32_t bt = t == 1 ? tile + b_lo : tile;
 #pragma unroll
-    for (int ks = 0; ks < KS; ++ks) {
-      umma_ts(d, at + 8 * ks, umma_desc(bt + step(ks), lbo), idesc, acc);
-      acc = true;
-    }
+    for (int ks = 0; ks < KS; ++ks)
+      umma_ts(d, a + (t == 2 ? A_LO : 0u) + 8 * ks, tile + (((t == 1 ? B_LO : 0u) + step(ks)) >> 4), IDESC,
+              t + ks > 0);
   }
 }
 
-template <int FORM, int DK, int DV>
+// T: activation type.  SAVE: the backward pass's recomputation, which writes w and the
+// state before each chunk instead of o and S_out.  (Both are template parameters for the
+// size of the loop's code: it is walked once per chunk, and from beyond the instruction
+// caches every instruction costs several cycles.)
+template <int FORM, int DK, int DV, typename T, bool SAVE>
 __global__ void __launch_bounds__(kNT, 1) scan_pass_kernel(const ScanParams p) {
   constexpr bool KDA = FORM == SEED_KDA, M2 = FORM == SEED_MAMBA2;
   using Sm = PassSmem<FORM, DK>;
@@ -166,15 +167,10 @@ __global__ void __launch_bounds__(kNT, 1) scan_pass_kernel(const ScanParams p) {
       const int par = c & 1;
       const long long first = sr.first + (long long)c * kChunk;
       const int n = min(kChunk, sr.len - c * kChunk);
-      auto load = [&](const void* src, int i, float (&x)[8]) {
-        float4 a = zero4(), b = zero4();
-        if (i < n) {
-          const long long at = ((first + i) * p.HK + hk) * DK + c0;
-          a = act_ld4(src, at, p.elem);
-          b = act_ld4(src, at + 4, p.elem);
-        }
-        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-        x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+      // this thread's values of q or k: rows r0, r0 + RPI, .., zeros behind the tokens
+      auto load = [&](const void* src, float (&x)[IT][8]) {
+        act_ld8_rows(static_cast<const T*>(src) + ((first + r0) * p.HK + hk) * DK + c0, (long long)RPI * p.HK * DK,
+                     (n - r0 + RPI - 1) / RPI, x);
       };
       // decays of the chunk and the per-token vectors
       if (t < kChunk) {
@@ -230,11 +226,14 @@ __global__ void __launch_bounds__(kNT, 1) scan_pass_kernel(const ScanParams p) {
       }
       const unsigned char* img = p.tri + ((long long)(sr.slot0 + c) * p.H + h) * kTriBytes;
       // row-scaled tiles: x (times the decays per channel) and what undoes the scale
-      auto rows = [&](const void* src, unsigned char* tile, float* cs, int bar, int full) {
+#pragma unroll 1
+      for (int which = M2 ? 1 : 0; which < 2; ++which) {      // Kb, then Qb
+        if (SAVE && which == 1) break;
+        unsigned char* tile = which ? sm.Q : sm.K;
+        float* cs = which ? sm.csQ[par] : sm.csK[par];
         float x[IT][8];
-#pragma unroll
-        for (int it = 0; it < IT; ++it) load(src, r0 + it * RPI, x[it]);
-        if (c >= 1) wait(bar, c - 1);
+        load(which ? p.q : p.k, x);
+        if (c >= 1) wait(which ? kBarQ : kBarK, c - 1);
 #pragma unroll
         for (int it = 0; it < IT; ++it) {
           const int i = r0 + it * RPI;
@@ -253,10 +252,8 @@ __global__ void __launch_bounds__(kNT, 1) scan_pass_kernel(const ScanParams p) {
           put(tile, i, x[it]);
         }
         fence_proxy_async_smem();
-        mbar_arrive(&sm.bar[full]);
-      };
-      if constexpr (!M2) rows(p.k, sm.K, sm.csK[par], kBarK, kFullK);
-      rows(p.q, sm.Q, sm.csQ[par], kBarQ, kFullQ);
+        mbar_arrive(&sm.bar[which ? kFullQ : kFullK]);
+      }
       if constexpr (!M2) {
         if (t == 0) {
           if (c >= 1) wait(kBarT, c - 1);
@@ -268,8 +265,7 @@ __global__ void __launch_bounds__(kNT, 1) scan_pass_kernel(const ScanParams p) {
       }
       {      // keys times the decays to the chunk's end, one scale for the tile
         float x[IT][8], m = 0.f;
-#pragma unroll
-        for (int it = 0; it < IT; ++it) load(p.k, r0 + it * RPI, x[it]);
+        load(p.k, x);
 #pragma unroll
         for (int it = 0; it < IT; ++it) {
           const int i = r0 + it * RPI;
@@ -304,7 +300,7 @@ __global__ void __launch_bounds__(kNT, 1) scan_pass_kernel(const ScanParams p) {
         if (c >= 1) wait(kBarDone, c - 1);
         mbar_arrive(&sm.bar[kFullH]);
       }
-      if (t == 0) {
+      if (!SAVE && t == 0) {
         if (c >= 1) wait(kBarP, c - 1);
         mbar_arrive_expect_tx(&sm.bar[kFullP], 16384 + kChunk * 4);
         bulk_g2s(sm.P, img + 16384, 16384, &sm.bar[kFullP]);
@@ -314,7 +310,7 @@ __global__ void __launch_bounds__(kNT, 1) scan_pass_kernel(const ScanParams p) {
     }
     if (t == 0 && sm.dead) {      // a wait ran out: let the copies in flight land all the same
       if (!M2) mbar_wait_bounded(&sm.bar[kFullT], (uint32_t)(nch - 1) & 1u, kWaitLimitNs);
-      mbar_wait_bounded(&sm.bar[kFullP], (uint32_t)(nch - 1) & 1u, kWaitLimitNs);
+      if (!SAVE) mbar_wait_bounded(&sm.bar[kFullP], (uint32_t)(nch - 1) & 1u, kWaitLimitNs);
     }
   } else {
     // ================================================================ lanes
@@ -331,191 +327,204 @@ __global__ void __launch_bounds__(kNT, 1) scan_pass_kernel(const ScanParams p) {
       pair_sync();
       return fmaxf(m, sm.mx[which][(half ^ 1) * 128 + j]);
     };
+    // 32 values in registers as the A operand at kRW, scaled by s
+    auto put_rw = [&](const float (&x)[32], float s) {
+      uint32_t hi[16], lo[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) split2(s * x[2 * e], s * x[2 * e + 1], hi[e], lo[e]);
+      tmem_st16(lanes + kRW + t0 / 2, hi);
+      tmem_st16(lanes + kRW + 32 + t0 / 2, lo);
+      tmem_wait_st();
+      tmem_fence_before();
+    };
+    constexpr uint32_t kIdesc64 = umma_idesc(128, 64, false), kIdescUp = umma_idesc(128, DK, true);
+    const auto rowstep = [](int ks) { return (uint32_t)((ks >> 2) * 8192 + (ks & 3) * 32); };
+    const long long vstep = (long long)p.H * DV;       // from a token's values to the next one's
     float S[NS];
 #pragma unroll
     for (int c = 0; c < NS; ++c) S[c] = on && p.S0 != nullptr ? p.S0[sh * mat + (long long)(cs0 + c) * DV + j] : 0.f;
-    bool bad = false;
-    float invS_prev = 1.f, invW = 1.f;
-    const bool want_o = p.o != nullptr;
+    float nan = 0.f, top = 0.f;      // NaN once a result was not finite; the largest |o|
+    float invS = 1.f, invW = 1.f;
 
-    // o of chunk c from its two accumulators
-    auto outputs = [&](int c, float invS, float invw) {
-      const long long first = sr.first + (long long)c * kChunk;
-      const int n = min(kChunk, sr.len - c * kChunk), par = c & 1;
-      wait(kBarP, c);
-      tmem_fence_after();
+    // one turn more than chunks: the last one only writes the last outputs
+    for (int c = 0; c < nch + (SAVE ? 0 : 1); ++c) {
+      const int par = c & 1;
+      float m = 0.f;
+      const float invS_before = invS;
+      if (c < nch && !(SAVE && M2)) {
+        // ---- S^T as an operand
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        float a[16], b[16];
-        tmem_ld16(lanes + kQS + t0 + 16 * x, a);
-        tmem_ld16(lanes + kPW + t0 + 16 * x, b);
-        tmem_wait_ld();
+        for (int x = 0; x < NS; ++x) m = fmaxf(m, fabsf(S[x]));
+        m = pair_max(m, 0);
+        const float sS = pow2_scale(m);
+        invS = pow2_inverse(sS);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const int i = t0 + 16 * x + e;
-          const float o = fmaf(a[e], invS * sm.csQ[par][i], b[e] * (invw * sm.invP[par][i]));
-          if (on && i < n) {
-            act_st(p.o, ((first + i) * p.H + h) * DV + j, o, p.elem);
-            bad = bad || !act_finite(o, p.elem);
+        for (int x = 0; x < NS / 32; ++x) {
+          uint32_t hi[16], lo[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) split2(sS * S[32 * x + 2 * e], sS * S[32 * x + 2 * e + 1], hi[e], lo[e]);
+          tmem_st16(lanes + kS + cs0 / 2 + 16 * x, hi);
+          tmem_st16(lanes + kS + 64 + cs0 / 2 + 16 * x, lo);
+        }
+        tmem_wait_st();
+        tmem_fence_before();
+        // A thread waits for a tile before the barrier behind which the products that free
+        // the tile are issued: every thread has seen the tile (and the vectors written with
+        // it) before its barrier can move on.
+        if constexpr (!M2) {
+          wait(kFullK, c);
+          lane_sync();
+          if (tid == 0) {
+            tmem_fence_after();
+            product<DK / 16, 64, TILE, kIdesc64>(tm + kKS, tm + kS, umma_desc(smem_addr(sm.K), 16), rowstep);
+            umma_commit(&sm.bar[kBarK]);
           }
         }
       }
-      tmem_fence_before();
-    };
-
-    for (int c = 0; c < nch; ++c) {
+      if constexpr (SAVE) {
+        if (on) {
+          float* dst = p.chunk_S + ((long long)(sr.slot0 + c) * p.H + h) * mat + (long long)cs0 * DV + j;
+#pragma unroll
+          for (int x = 0; x < NS; ++x) dst[x * DV] = S[x];
+        }
+      } else if (c > 0) {
+        // ---- the last chunk's outputs, beside this one's S^T Kb^T
+        const int before = par ^ 1, n = min(kChunk, sr.len - (c - 1) * kChunk);
+        wait(kBarP, c - 1);
+        tmem_fence_after();
+#pragma unroll 1
+        for (int x = t0; x < t0 + 32; x += 16) {
+          float a[16], b[16];
+          tmem_ld16(lanes + kQS + x, a);
+          tmem_ld16(lanes + kPW + x, b);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 16; e += 4) {
+            const float4 fq = ld4(&sm.csQ[before][x + e]), fp = ld4(&sm.invP[before][x + e]);
+            a[e] = fmaf(a[e], invS_before * fq.x, b[e] * (invW * fp.x));
+            a[e + 1] = fmaf(a[e + 1], invS_before * fq.y, b[e + 1] * (invW * fp.y));
+            a[e + 2] = fmaf(a[e + 2], invS_before * fq.z, b[e + 2] * (invW * fp.z));
+            a[e + 3] = fmaf(a[e + 3], invS_before * fq.w, b[e + 3] * (invW * fp.w));
+          }
+          if (on) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {      // (tokens behind the chunk's have q = 0 and rows of P of zeros)
+              nan = fmaf(a[e], 0.f, nan);
+              top = fmaxf(top, fabsf(a[e]));
+            }
+            act_st_rows(static_cast<T*>(p.o) + ((sr.first + (long long)(c - 1) * kChunk + x) * p.H + h) * DV + j, vstep,
+                        n - x, a);
+          }
+        }
+        tmem_fence_before();
+      }
+      if (c > 0) mbar_arrive(&sm.bar[kBarDone]);
+      if (c == nch) break;
       const long long first = sr.first + (long long)c * kChunk;
-      const int n = min(kChunk, sr.len - c * kChunk), par = c & 1;
-      // ---- S^T as an operand
-      float m = 0.f;
-#pragma unroll
-      for (int x = 0; x < NS; ++x) m = fmaxf(m, fabsf(S[x]));
-      m = pair_max(m, 0);
-      const float sS = pow2_scale(m), invS = pow2_inverse(sS);
-#pragma unroll
-      for (int x = 0; x < NS / 32; ++x) {
-        uint32_t hi[16], lo[16];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) split2(sS * S[32 * x + 2 * e], sS * S[32 * x + 2 * e + 1], hi[e], lo[e]);
-        tmem_st16(lanes + kS + cs0 / 2 + 16 * x, hi);
-        tmem_st16(lanes + kS + 64 + cs0 / 2 + 16 * x, lo);
-      }
-      tmem_wait_st();
-      tmem_fence_before();
-      // A thread waits for a tile before the barrier behind which the products that free
-      // the tile are issued: every thread has seen the tile (and the vectors written with
-      // it) before its barrier can move on.
-      if constexpr (!M2) wait(kFullK, c);
-      lane_sync();
-      const auto rowstep = [](int ks) { return (uint32_t)((ks >> 2) * 8192 + (ks & 3) * 32); };
-      if (!M2 && tid == 0) {
-        tmem_fence_after();
-        product<DK / 16>(tm + kKS, tm + kS, 64, smem_addr(sm.K), TILE, 16, umma_idesc(128, 64, false), rowstep);
-        umma_commit(&sm.bar[kBarK]);
-      }
-      if (p.chunk_S != nullptr && on) {
-        float* dst = p.chunk_S + ((long long)(sr.slot0 + c) * p.H + h) * mat + (long long)cs0 * DV + j;
-#pragma unroll
-        for (int x = 0; x < NS; ++x) dst[(long long)x * DV] = S[x];
-      }
-      // ---- the last chunk's outputs, then this one's S^T Qb^T
-      if (c > 0) {
-        if (want_o) outputs(c - 1, invS_prev, invW);
-        mbar_arrive(&sm.bar[kBarDone]);
-      }
-      wait(kFullQ, c);
-      lane_sync();
-      if (tid == 0) {
-        tmem_fence_after();
-        if (want_o)
-          product<DK / 16>(tm + kQS, tm + kS, 64, smem_addr(sm.Q), TILE, 16, umma_idesc(128, 64, false), rowstep);
-        umma_commit(&sm.bar[kBarQ]);
+      const int n = min(kChunk, sr.len - c * kChunk);
+      if constexpr (!SAVE) {
+        wait(kFullQ, c);
+        lane_sync();
+        if (tid == 0) {
+          tmem_fence_after();
+          product<DK / 16, 64, TILE, kIdesc64>(tm + kQS, tm + kS, umma_desc(smem_addr(sm.Q), 16), rowstep);
+          umma_commit(&sm.bar[kBarQ]);
+        }
       }
       // ---- r, w
       float x[32];
-#pragma unroll
-      for (int e = 0; e < 32; ++e)
-        x[e] = on && t0 + e < n ? act_ld(p.v, ((first + t0 + e) * p.H + h) * DV + j, p.elem) : 0.f;
+      act_ld_rows(static_cast<const T*>(p.v) + ((first + t0) * p.H + h) * DV + j, vstep, on ? n - t0 : 0, x);
       if constexpr (!M2) {
         wait(kBarK, c);
         tmem_fence_after();
         m = 0.f;
 #pragma unroll
-        for (int y = 0; y < 2; ++y) {
+        for (int y = 0; y < 32; y += 16) {
           float a[16];
-          tmem_ld16(lanes + kKS + t0 + 16 * y, a);
+          tmem_ld16(lanes + kKS + t0 + y, a);
           tmem_wait_ld();
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const int i = t0 + 16 * y + e;
-            x[16 * y + e] = sm.beta[par][i] * fmaf(-a[e], invS * sm.csK[par][i], x[16 * y + e]);
-            m = fmaxf(m, fabsf(x[16 * y + e]));
+          for (int e = 0; e < 16; e += 4) {
+            const float4 fk = ld4(&sm.csK[par][t0 + y + e]), be = ld4(&sm.beta[par][t0 + y + e]);
+            x[y + e] = be.x * fmaf(-a[e], invS * fk.x, x[y + e]);
+            x[y + e + 1] = be.y * fmaf(-a[e + 1], invS * fk.y, x[y + e + 1]);
+            x[y + e + 2] = be.z * fmaf(-a[e + 2], invS * fk.z, x[y + e + 2]);
+            x[y + e + 3] = be.w * fmaf(-a[e + 3], invS * fk.w, x[y + e + 3]);
           }
         }
+#pragma unroll
+        for (int e = 0; e < 32; ++e) m = fmaxf(m, fabsf(x[e]));
         m = pair_max(m, 1);
         const float sR = pow2_scale(m), invR = pow2_inverse(sR);
-        uint32_t hi[16], lo[16];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) split2(sR * x[2 * e], sR * x[2 * e + 1], hi[e], lo[e]);
-        tmem_st16(lanes + kRW + t0 / 2, hi);
-        tmem_st16(lanes + kRW + 32 + t0 / 2, lo);
-        tmem_wait_st();
-        tmem_fence_before();
+        put_rw(x, sR);
         wait(kFullT, c);
         lane_sync();
         if (tid == 0) {
           tmem_fence_after();
-          product<4>(tm + kKS, tm + kRW, 32, smem_addr(sm.T), 8192, 16, umma_idesc(128, 64, false),
-                     [](int ks) { return (uint32_t)(ks * 32); });
+          product<4, 32, 8192, kIdesc64>(tm + kKS, tm + kRW, umma_desc(smem_addr(sm.T), 16), rowstep);
           umma_commit(&sm.bar[kBarT]);
         }
         wait(kBarT, c);
         tmem_fence_after();
-#pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          tmem_ld16(lanes + kKS + t0 + 16 * y, x + 16 * y);
-        }
+        tmem_ld16(lanes + kKS + t0, x);
+        tmem_ld16(lanes + kKS + t0 + 16, x + 16);
         tmem_wait_ld();
 #pragma unroll
-        for (int e = 0; e < 32; ++e) x[e] *= invR * sm.invT[par][t0 + e];
+        for (int e = 0; e < 32; e += 4) {
+          const float4 ft = ld4(&sm.invT[par][t0 + e]);
+          x[e] *= invR * ft.x;
+          x[e + 1] *= invR * ft.y;
+          x[e + 2] *= invR * ft.z;
+          x[e + 3] *= invR * ft.w;
+        }
       } else {
+        if constexpr (SAVE) wait(kFullH, c);      // the vectors come with the first tile
 #pragma unroll
-        for (int e = 0; e < 32; ++e) x[e] *= sm.beta[par][t0 + e];
+        for (int e = 0; e < 32; e += 4) {
+          const float4 be = ld4(&sm.beta[par][t0 + e]);
+          x[e] *= be.x;
+          x[e + 1] *= be.y;
+          x[e + 2] *= be.z;
+          x[e + 3] *= be.w;
+        }
       }
-      if (p.w != nullptr && on) {
-        float* dst = p.w + ((first + t0) * p.H + h) * DV + j;
-#pragma unroll
-        for (int e = 0; e < 32; ++e)
-          if (t0 + e < n) dst[(long long)e * p.H * DV] = x[e];
-      }
+      if constexpr (SAVE) act_st_rows(p.w + ((first + t0) * p.H + h) * DV + j, vstep, on ? n - t0 : 0, x);
       m = 0.f;
 #pragma unroll
       for (int e = 0; e < 32; ++e) m = fmaxf(m, fabsf(x[e]));
       m = pair_max(m, 0);
       const float sW = pow2_scale(m);
       invW = pow2_inverse(sW);
-      {
-        uint32_t hi[16], lo[16];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) split2(sW * x[2 * e], sW * x[2 * e + 1], hi[e], lo[e]);
-        tmem_st16(lanes + kRW + t0 / 2, hi);
-        tmem_st16(lanes + kRW + 32 + t0 / 2, lo);
-      }
-      tmem_wait_st();
-      tmem_fence_before();
+      put_rw(x, sW);
       wait(kFullH, c);
-      wait(kFullP, c);
+      if constexpr (!SAVE) wait(kFullP, c);
       lane_sync();
       if (tid == 0) {
         tmem_fence_after();
-        product<4>(tm + kUp, tm + kRW, 32, smem_addr(sm.H), TILE, 8192, umma_idesc(128, DK, true),
-                   [](int ks) { return (uint32_t)(ks * 2048); });
+        product<4, 32, TILE, kIdescUp>(tm + kUp, tm + kRW, umma_desc(smem_addr(sm.H), 8192),
+                                       [](int ks) { return (uint32_t)(ks * 2048); });
         umma_commit(&sm.bar[kBarH]);
-        if (want_o)
-          product<4>(tm + kPW, tm + kRW, 32, smem_addr(sm.P), 8192, 16, umma_idesc(128, 64, false),
-                     [](int ks) { return (uint32_t)(ks * 32); });
-        umma_commit(&sm.bar[kBarP]);
+        if constexpr (!SAVE) {
+          product<4, 32, 8192, kIdesc64>(tm + kPW, tm + kRW, umma_desc(smem_addr(sm.P), 16), rowstep);
+          umma_commit(&sm.bar[kBarP]);
+        }
       }
       // ---- S behind the chunk
       wait(kBarH, c);
       tmem_fence_after();
-      const float up = invW * sm.invH[par];
+      const float up = invW * sm.invH[par], end = sm.end[par][0];
 #pragma unroll
-      for (int y = 0; y < NS / 16; ++y) {
+      for (int y = 0; y < NS; y += 16) {
         float a[16];
-        tmem_ld16(lanes + kUp + cs0 + 16 * y, a);
+        tmem_ld16(lanes + kUp + cs0 + y, a);
         tmem_wait_ld();
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const float d = KDA ? sm.end[par][cs0 + 16 * y + e] : sm.end[par][0];
-          S[16 * y + e] = fmaf(a[e], up, d * S[16 * y + e]);
-        }
+        for (int e = 0; e < 16; ++e) S[y + e] = fmaf(a[e], up, (KDA ? sm.end[par][cs0 + y + e] : end) * S[y + e]);
       }
       tmem_fence_before();
-      invS_prev = invS;
     }
-    if (want_o) outputs(nch - 1, invS_prev, invW);
-    if (p.S_out != nullptr && on) {
+    bool bad = !(nan == 0.f) || !act_finite(top, p.elem);
+    if (!SAVE && p.S_out != nullptr && on) {
       float* dst = p.S_out + sh * mat + (long long)cs0 * DV + j;
 #pragma unroll
       for (int c = 0; c < NS; ++c) {
@@ -524,9 +533,7 @@ __global__ void __launch_bounds__(kNT, 1) scan_pass_kernel(const ScanParams p) {
       }
     }
     if (bad) raise_flag(p.status, SEED_FLAG_NONFINITE);
-    // nothing of this block is in flight when it ends: the last products were waited for
-    // (or waited for in vain above), and with them the copies they read
-    wait(kBarP, nch - 1);
+    // every product was waited for, and with it the copies it read
     tmem_fence_before();
   }
   __syncthreads();
@@ -536,7 +543,7 @@ __global__ void __launch_bounds__(kNT, 1) scan_pass_kernel(const ScanParams p) {
   }
 }
 
-template <int FORM, int DK, int DV>
+template <int FORM, int DK, int DV, typename T, bool SAVE>
 int launch_pass_t(const ScanParams& p, cudaStream_t st) {
   static LaunchCache cache;
   // one block per SM (it holds all of the SM's tensor memory)
@@ -544,16 +551,20 @@ int launch_pass_t(const ScanParams& p, cudaStream_t st) {
   constexpr size_t bytes = need < 116 * 1024 ? 116 * 1024 : need;
   static_assert(bytes <= 227 * 1024, "shared memory");
   int dev;
-  if (int rc = cache.prepare(reinterpret_cast<const void*>(scan_pass_kernel<FORM, DK, DV>), bytes, &dev)) return rc;
-  scan_pass_kernel<FORM, DK, DV><<<p.seqs * p.H, kNT, bytes, st>>>(p);
+  if (int rc = cache.prepare(reinterpret_cast<const void*>(scan_pass_kernel<FORM, DK, DV, T, SAVE>), bytes, &dev))
+    return rc;
+  scan_pass_kernel<FORM, DK, DV, T, SAVE><<<p.seqs * p.H, kNT, bytes, st>>>(p);
   return cudaGetLastError() == cudaSuccess ? SEED_OK : SEED_ERR_CUDA;
 }
 
 }  // namespace
 
-int launch_scan_pass(const ScanParams& p, int form, cudaStream_t st) {
-#define SEED_PASS(F, K, V) \
-  if (form == F && p.dk == K && p.dv == V) return launch_pass_t<F, K, V>(p, st);
+// The launcher for one activation type (instantiated by seed_scan_pass_*.cu).
+template <typename T>
+int launch_scan_pass_as(const ScanParams& p, int form, cudaStream_t st) {
+#define SEED_PASS(F, K, V)                                                                       \
+  if (form == F && p.dk == K && p.dv == V)                                                       \
+    return p.chunk_S != nullptr ? launch_pass_t<F, K, V, T, true>(p, st) : launch_pass_t<F, K, V, T, false>(p, st);
 #define SEED_PASS_D(F) SEED_PASS(F, 64, 64) SEED_PASS(F, 128, 128) SEED_PASS(F, 128, 64) SEED_PASS(F, 64, 128)
   SEED_PASS_D(SEED_GDN)
   SEED_PASS_D(SEED_KDA)

@@ -192,19 +192,23 @@ __global__ void __launch_bounds__(kNT) scan_prep_kernel(const ScanParams p) {
   const int n = ck.n;
   const int hk = KDA ? grp / rep : grp;
 
-  for (int e = tid; e < kChunk * DK / 4; e += kNT) {
-    const int i = e / (DK / 4), c = 4 * (e % (DK / 4));
-    float4 q = zero4(), k = zero4(), a = make_float4(1.f, 1.f, 1.f, 1.f);
-    if (i < n) {
-      const long long at = ((ck.first + i) * p.HK + hk) * DK + c;
-      q = act_ld4(p.q, at, p.elem);
-      k = act_ld4(p.k, at, p.elem);
-      if constexpr (KDA) a = ld4(p.alpha + ((ck.first + i) * p.H + grp) * DK + c);
+  act_type(p.elem, [&](auto tag) {
+    using E = decltype(tag);
+#pragma unroll
+    for (int e = tid; e < kChunk * DK / 4; e += kNT) {
+      const int i = e / (DK / 4), c = 4 * (e % (DK / 4));
+      float4 q = zero4(), k = zero4(), a = make_float4(1.f, 1.f, 1.f, 1.f);
+      if (i < n) {
+        const long long at = ((ck.first + i) * p.HK + hk) * DK + c;
+        q = fac_ld4(static_cast<const E*>(p.q) + at);
+        k = fac_ld4(static_cast<const E*>(p.k) + at);
+        if constexpr (KDA) a = ld4(p.alpha + ((ck.first + i) * p.H + grp) * DK + c);
+      }
+      st4(&sm.in.q[i * PK + c], q);
+      st4(&sm.in.k[i * PK + c], k);
+      if constexpr (KDA) st4(&sm.in.a[i * PK + c], a);
     }
-    st4(&sm.in.q[i * PK + c], q);
-    st4(&sm.in.k[i * PK + c], k);
-    if constexpr (KDA) st4(&sm.in.a[i * PK + c], a);
-  }
+  });
   __syncthreads();
 
   if constexpr (!KDA) {

@@ -43,21 +43,24 @@ struct StepRegs {
   // tokens t0 .. t0 + n - 1 of the sequence (n <= kStage), forward order
   SEED_DEV void load(const ScanParams& p, long long row0, int n, int h, int col0, const void* xs, int tid) {
     const int hk = h / (p.H / p.HK);
+    act_type(p.elem, [&](auto tag) {
+      using T = decltype(tag);
 #pragma unroll
-    for (int m = 0; m < PER; ++m) {
-      const int e = tid + m * kNT;
-      const int t = e / (DK / 4), c = 4 * (e % (DK / 4));
-      if (e < V4 && t < n) {
-        const long long at = ((row0 + t) * p.HK + hk) * DK + c;
-        k[m] = act_ld4(p.k, at, p.elem);
-        q[m] = act_ld4(p.q, at, p.elem);
-        if constexpr (FORM == SEED_KDA) a[m] = ld4(p.alpha + ((row0 + t) * p.H + h) * DK + c);
+      for (int m = 0; m < PER; ++m) {
+        const int e = tid + m * kNT;
+        const int t = e / (DK / 4), c = 4 * (e % (DK / 4));
+        if (e < V4 && t < n) {
+          const long long at = ((row0 + t) * p.HK + hk) * DK + c;
+          k[m] = fac_ld4(static_cast<const T*>(p.k) + at);
+          q[m] = fac_ld4(static_cast<const T*>(p.q) + at);
+          if constexpr (FORM == SEED_KDA) a[m] = ld4(p.alpha + ((row0 + t) * p.H + h) * DK + c);
+        }
       }
-    }
-    if (tid < kStage * kCols / 4) {
-      const int t = tid / (kCols / 4), c = col0 + 4 * (tid % (kCols / 4));
-      if (t < n && c < p.dv) x = act_ld4(xs, ((row0 + t) * p.H + h) * p.dv + c, p.elem);
-    }
+      if (tid < kStage * kCols / 4) {
+        const int t = tid / (kCols / 4), c = col0 + 4 * (tid % (kCols / 4));
+        if (t < n && c < p.dv) x = fac_ld4(static_cast<const T*>(xs) + ((row0 + t) * p.H + h) * p.dv + c);
+      }
+    });
     if (tid < n) {
       const long long at = (row0 + tid) * p.H + h;
       b1 = p.beta[at];
