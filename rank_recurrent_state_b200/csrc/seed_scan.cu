@@ -31,7 +31,11 @@ bool chunked(const ScanParams& p, const seed_scan_dims& d) {
 size_t carve(ScanParams& p, const seed_scan_dims& d, bool backward, void* ws) {
   Carver c;
   c.base = static_cast<unsigned char*>(ws);
-  if (chunked(p, d)) p.tri = c.take<unsigned char>((long long)p.slots * p.H * kTriBytes);
+  if (chunked(p, d)) {
+    const bool two = scan_two_terms(d.form, d.elem == SEED_FACTORS_F32);
+    p.tri = c.take<unsigned char>((long long)p.slots * p.H * kTriBytes);
+    p.kq = c.take<unsigned char>((long long)p.slots * (d.form == SEED_KDA ? p.H : p.HK) * kq_bytes(d.form, p.dk, two));
+  }
   if (backward) {
     const long long rows = p.tokens * p.H, mats = (long long)p.slots * p.H * p.dk * p.dv;
     p.w = c.take<float>(rows * p.dv);
@@ -46,10 +50,13 @@ size_t carve(ScanParams& p, const seed_scan_dims& d, bool backward, void* ws) {
 // Forward, or its recomputation: o, S_out, w and chunk_S where they are asked for.
 int forward(const ScanParams& p, const seed_scan_dims& d, cudaStream_t st) {
   if (!chunked(p, d)) return launch_scan_step(p, d.form, st);
-  if (d.tokens > 0) {
-    if (const int rc = launch_scan_prep(p, d.form, st)) return rc;
-  }
-  return with_factor_type_of(d.elem, [&](auto t) -> int { return launch_scan_pass_as<decltype(t)>(p, d.form, st); });
+  return with_factor_type_of(d.elem, [&](auto t) -> int {
+    using T = decltype(t);
+    if (d.tokens > 0) {
+      if (const int rc = launch_scan_prep_as<T>(p, d.form, st)) return rc;
+    }
+    return launch_scan_pass_as<T>(p, d.form, st);
+  });
 }
 
 ScanParams params_of(const seed_scan_dims& d) {

@@ -14,9 +14,24 @@
 namespace seed {
 
 constexpr int kChunk = 64;
-// Scratch of one chunk and head for the chunked passes: the images of T and P (two fp16
-// terms of 64 x 64 each) and their rows' scales.
-constexpr int kTriBytes = 4 * 8192 + 2 * kChunk * 4;
+// ---- Scratch of the chunked passes, as seed_scan_prep.cuh writes it.
+// Per chunk and head: T and P (two fp16 terms of 64 x 64 each), then vectors of 64
+// floats, then the product of the chunk's decays (one, or one per channel).
+constexpr int kTriVec = 4 * 8192;
+enum { kVecT, kVecP,      // what undoes the scales of T's and P's rows
+       kVecK, kVecQ,      // the same for the k and q rows, times B_i where the tiles have no decay in them
+       kVecE,             // for the k rows of the state's update, times E_i likewise
+       kVecBeta, kVecs };
+constexpr int kTriEnd = kTriVec + kVecs * kChunk * 4;
+constexpr int kTriBytes = kTriEnd + 512;
+constexpr int kVecBytes = kTriBytes - kTriVec;
+// Per chunk and key head (decays per channel: per chunk and head): the k rows, then the q
+// rows, in panels of 64 channels; a second fp16 term where one does not hold the values;
+// with decays per channel the tile of E k behind them.
+__host__ __device__ constexpr bool scan_two_terms(int form, bool f32) { return f32 || form == SEED_KDA; }
+__host__ __device__ constexpr int kq_bytes(int form, int dk, bool two) {
+  return (two ? 2 : 1) * dk * 256 + (form == SEED_KDA ? dk * 256 : 0);
+}
 
 struct ScanParams {
   const int32_t* offsets;
@@ -44,6 +59,7 @@ struct ScanParams {
   float* chunk_dS;        // [slots][H][dk][dv]: the gradient of the state behind each chunk
   float* part;            // [2][tokens][H][dk]: dq and dk per value head where heads share keys
   unsigned char* tri;     // [slots][H][kTriBytes]
+  unsigned char* kq;      // [slots][HK, KDA: H][kq_bytes]
   uint32_t* status;
   long long tokens;
   int seqs, H, HK, dk, dv, elem, slots;
@@ -192,8 +208,9 @@ SEED_DEV bool chunk_at(const ScanParams& p, int slot, ChunkAt* c) {
 // Token-by-token kernels (seed_scan_step.cu).
 int launch_scan_step(const ScanParams& p, int form, cudaStream_t st);
 int launch_scan_step_back(const ScanParams& p, int form, cudaStream_t st);
-// T and P of every chunk (seed_scan_prep.cu), d_k in {64, 128}.
-int launch_scan_prep(const ScanParams& p, int form, cudaStream_t st);
+// What the passes need of every chunk (seed_scan_prep.cuh), d_k in {64, 128}.
+template <typename T>
+int launch_scan_prep_as(const ScanParams& p, int form, cudaStream_t st);
 // The chunked pass on the tensor cores for activations of type T (seed_scan_pass.cuh),
 // d_k and d_v in {64, 128}; writes w and chunk_S instead of o and S_out where chunk_S is set.
 template <typename T>

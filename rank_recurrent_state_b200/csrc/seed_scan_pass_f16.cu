@@ -1,9 +1,12 @@
-// seed_scan_pass_f16.cu -- the chunked pass of the dense scan for __half activations
-// (kernel in seed_scan_pass.cuh; one file per type, so that they compile in parallel).
+// seed_scan_pass_f16.cu -- the chunked kernels of the dense scan for __half activations
+// (seed_scan_prep.cuh, seed_scan_pass.cuh; one file per type, so that they compile in
+// parallel).
 #include "seed_scan_pass.cuh"
+#include "seed_scan_prep.cuh"
 
 namespace seed {
 
+template int launch_scan_prep_as<__half>(const ScanParams& p, int form, cudaStream_t st);
 template int launch_scan_pass_as<__half>(const ScanParams& p, int form, cudaStream_t st);
 
 }  // namespace seed

@@ -1,9 +1,12 @@
-// seed_scan_pass_f32.cu -- the chunked pass of the dense scan for float activations
-// (kernel in seed_scan_pass.cuh; one file per type, so that they compile in parallel).
+// seed_scan_pass_f32.cu -- the chunked kernels of the dense scan for float activations
+// (seed_scan_prep.cuh, seed_scan_pass.cuh; one file per type, so that they compile in
+// parallel).
 #include "seed_scan_pass.cuh"
+#include "seed_scan_prep.cuh"
 
 namespace seed {
 
+template int launch_scan_prep_as<float>(const ScanParams& p, int form, cudaStream_t st);
 template int launch_scan_pass_as<float>(const ScanParams& p, int form, cudaStream_t st);
 
 }  // namespace seed
