@@ -103,16 +103,16 @@ template <typename T, int N>
 SEED_DEV void act_ld_rows(const T* src, long long step, int left, float (&x)[N]) {
   if constexpr (std::is_same<T, float>::value) {
 #pragma unroll
-    for (int e = 0; e < N; ++e) {
+    for (int e = 0; e < N; ++e, src += step) {
       x[e] = 0.f;
-      if (e < left) x[e] = src[e * step];
+      if (e < left) x[e] = *src;
     }
   } else {
     uint16_t raw[N];
 #pragma unroll
-    for (int e = 0; e < N; ++e) {
+    for (int e = 0; e < N; ++e, src += step) {
       raw[e] = 0;
-      if (e < left) raw[e] = reinterpret_cast<const uint16_t*>(src)[e * step];
+      if (e < left) raw[e] = *reinterpret_cast<const uint16_t*>(src);
     }
 #pragma unroll
     for (int e = 0; e < N; ++e) {
@@ -129,8 +129,8 @@ SEED_DEV void act_st_rows(T* dst, long long step, int left, const float (&x)[N])
 #pragma unroll
   for (int e = 0; e < N; ++e) t[e] = fac_from_f<T>(x[e]);
 #pragma unroll
-  for (int e = 0; e < N; ++e)
-    if (e < left) dst[e * step] = t[e];
+  for (int e = 0; e < N; ++e, dst += step)
+    if (e < left) *dst = t[e];
 }
 // N groups of eight consecutive values, `step` elements apart.
 template <typename T, int N>

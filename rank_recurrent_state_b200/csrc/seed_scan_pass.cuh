@@ -13,11 +13,12 @@
 // to there), T and P, MN-major for k in the update.  All products run in two-term fp16
 // (seed_umma.cuh); tiles of one term take two products instead of three.
 //
-// Warps 0-7 own the lanes (two warps per 32 lanes, half of the columns each) and thread 0
-// issues the products.  Warps 8-11 write the outputs, beside the next chunk's work, and
-// their first thread keeps the tiles coming (bulk copies, two chunks ahead where shared
-// memory holds two).  The chain per chunk is S -> r -> w -> S, three products and the
-// conversions between them; everything else hangs beside it.
+// Warps 0-7 own the lanes (two warps per 32 lanes, half of the columns each).  Warps 8-11
+// write the outputs, beside the next chunk's work.  Of warps 12-15, which give their
+// registers to the others, one thread issues the products and one keeps the tiles coming
+// (bulk copies, two chunks ahead where shared memory holds two).  The chain per chunk is
+// S -> r -> w -> S, three products and the conversions between them; everything else
+// hangs beside it.
 //
 // Waits are bounded: one that runs out raises SEED_FLAG_TIMEOUT, and every later wait of
 // the block returns at once, so that it ends (with unspecified results).
@@ -32,7 +33,10 @@ namespace {
 
 constexpr int kLaneThreads = 256;
 constexpr int kOutThreads = 128;
-constexpr int kPassThreads = kLaneThreads + kOutThreads;
+constexpr int kPassThreads = kLaneThreads + kOutThreads + 128;
+// Registers per thread of the lanes, the outputs and the rest; the launch gives each of the
+// 512 threads 128, and the shares stay within that: 2 x 160 + 144 + 48 = 4 x 128.
+constexpr int kLaneRegs = 160, kOutRegs = 144, kRestRegs = 48;
 
 // Tensor-memory columns (512 in all).
 constexpr uint32_t kS = 0;          // S^T: 64 columns hi, 64 lo; behind the first product (E w)^T: 32 hi, 32 lo
@@ -41,18 +45,21 @@ constexpr uint32_t kRW = 256;       // r^T, then w^T: 32 columns hi, 32 lo
 constexpr uint32_t kUp = 320;       // (E w)^T k (d_k)
 constexpr uint32_t kPW = 448;       // w^T P^T (64)
 
-template <int FORM, int DK, bool TWO>
+template <int FORM, int DK, int DV, typename T>
 struct PassSmem {
   static constexpr bool KDA = FORM == SEED_KDA, M2 = FORM == SEED_MAMBA2;
-  static constexpr int NST = KDA ? 1 : 2;               // chunks of tiles held
+  static constexpr bool TWO = scan_two_terms(FORM, std::is_same<T, float>::value);
+  static constexpr int NKQ = KDA ? 1 : 2;               // chunks of k and q tiles held
+  static constexpr int NTP = TWO ? 1 : 2;               // of T and P
   static constexpr int TERM = DK * 256;                 // one term of the k and q rows
   static constexpr int KQ = (TWO ? 2 : 1) * TERM;
-  struct Stage {
-    alignas(1024) unsigned char kq[KQ];
-    alignas(1024) unsigned char ke[KDA ? TERM : 1024];  // E k (two terms), decays per channel only
-    alignas(1024) unsigned char T[16384];
-    alignas(1024) unsigned char P[16384];
-  } st[NST];
+  static constexpr int OROWS = 32;                      // tokens of outputs staged at a time
+  alignas(1024) unsigned char kq[NKQ][KQ];
+  alignas(1024) unsigned char ke[KDA ? TERM : 1024];    // E k (two terms), decays per channel only
+  alignas(1024) unsigned char tt[NTP][M2 ? 1024 : 16384];
+  alignas(1024) unsigned char pp[NTP][16384];
+  alignas(128) T v[kChunk * DV];
+  alignas(128) T o[OROWS * DV];
   struct Vec {
     alignas(128) float v[kVecs][kChunk];
     float end[128];
@@ -62,9 +69,12 @@ struct PassSmem {
   // products done: accumulator ready, tiles free
   uint64_t done_kq, done_t, done_up, done_pw;
   // copies done
-  uint64_t full_kq[NST], full_ke[NST], full_t[NST], full_p[NST], full_vec[3];
+  uint64_t full_kq[NKQ], full_ke, full_t[NTP], full_p[NTP], full_vec[3], full_v;
   // the outputs have read an accumulator
   uint64_t free_q, free_pw;
+  uint64_t free_copy;             // the copying thread has seen a chunk's last product
+  // the lanes have stored an operand (one arrival per warp)
+  uint64_t op_s, op_r, op_e, op_w;
   uint32_t tmem;
   int dead;
 };
@@ -90,11 +100,14 @@ SEED_DEV void pass_wait(uint64_t* bar, uint32_t phase, volatile int* dead, uint3
 // for a tile of two terms, hi lo.  KS steps of 16, step(ks) bytes apart in the tile.
 template <int KS, bool TWO, uint32_t IDESC, typename Step>
 SEED_DEV void product(uint32_t d, uint32_t a, uint32_t a_lo, uint64_t tile, uint32_t b_lo, bool accumulate, Step step) {
+  const uint64_t high = tile & 0xffffffff00000000ull;
+  uint32_t low = (uint32_t)tile;
+  asm volatile("" : "+r"(low));      // or every step's descriptor is kept in a register across the chunks
 #pragma unroll
   for (int t = 0; t < (TWO ? 3 : 2); ++t) {
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks)
-      umma_ts(d, a + (t == 1 ? a_lo : 0u) + 8 * ks, tile + (((t == 2 ? b_lo : 0u) + step(ks)) >> 4), IDESC,
+      umma_ts(d, a + (t == 1 ? a_lo : 0u) + 8 * ks, high | (low + (((t == 2 ? b_lo : 0u) + step(ks)) >> 4)), IDESC,
               accumulate || t + ks > 0);
   }
 }
@@ -106,9 +119,9 @@ SEED_DEV void product(uint32_t d, uint32_t a, uint32_t a_lo, uint64_t tile, uint
 template <int FORM, int DK, int DV, typename T, bool SAVE>
 __global__ void __launch_bounds__(kPassThreads, 1) scan_pass_kernel(const ScanParams p) {
   constexpr bool KDA = FORM == SEED_KDA, M2 = FORM == SEED_MAMBA2;
-  constexpr bool TWO = scan_two_terms(FORM, std::is_same<T, float>::value);
-  using Sm = PassSmem<FORM, DK, TWO>;
-  constexpr int NST = Sm::NST;
+  using Sm = PassSmem<FORM, DK, DV, T>;
+  constexpr bool TWO = Sm::TWO;
+  constexpr int NKQ = Sm::NKQ, NTP = Sm::NTP;
   constexpr uint32_t TERM = Sm::TERM;
   extern __shared__ unsigned char smem_raw[];
   Sm& sm = *reinterpret_cast<Sm*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
@@ -131,15 +144,21 @@ __global__ void __launch_bounds__(kPassThreads, 1) scan_pass_kernel(const ScanPa
     mbar_init(&sm.done_t, 1);
     mbar_init(&sm.done_up, 1);
     mbar_init(&sm.done_pw, 1);
-    for (int s = 0; s < NST; ++s) {
-      mbar_init(&sm.full_kq[s], 1);
-      mbar_init(&sm.full_ke[s], 1);
+    for (int s = 0; s < NKQ; ++s) mbar_init(&sm.full_kq[s], 1);
+    for (int s = 0; s < NTP; ++s) {
       mbar_init(&sm.full_t[s], 1);
       mbar_init(&sm.full_p[s], 1);
     }
+    mbar_init(&sm.full_ke, 1);
+    mbar_init(&sm.full_v, 1);
     for (int s = 0; s < 3; ++s) mbar_init(&sm.full_vec[s], 1);
-    mbar_init(&sm.free_q, kOutThreads);
-    mbar_init(&sm.free_pw, kOutThreads);
+    mbar_init(&sm.free_q, kOutThreads / 32);
+    mbar_init(&sm.free_pw, kOutThreads / 32);
+    mbar_init(&sm.free_copy, 1);
+    mbar_init(&sm.op_s, kLaneThreads / 32);
+    mbar_init(&sm.op_r, kLaneThreads / 32);
+    mbar_init(&sm.op_e, kLaneThreads / 32);
+    mbar_init(&sm.op_w, kLaneThreads / 32);
     fence_mbar_init();
     sm.dead = 0;
   }
@@ -154,57 +173,151 @@ __global__ void __launch_bounds__(kPassThreads, 1) scan_pass_kernel(const ScanPa
   const bool on = j < DV;
   const uint32_t lanes = tm + ((uint32_t)(32 * lg) << 16);
   const long long vstep = (long long)p.H * DV;       // from a token's values to the next one's
-  // No barrier runs two phases ahead of a thread that waits for it: done_kq and done_pw of
-  // a chunk need free_q and free_pw of the one before, which every output thread signals
-  // behind its own waits; done_t and done_up need the lanes' block barriers; a tile's
-  // barrier has thread 0 as its only waiter; the vectors' come round every third chunk.
+  auto warp_arrive = [&](uint64_t* bar) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
+  };
+  // No barrier runs two phases ahead of a thread that waits for it.  The products of a
+  // chunk wait for the lanes' operands of that chunk, and the first and the last one for
+  // the outputs of the chunk before (free_q, free_pw); lanes and outputs signal behind
+  // their own waits.  The issuing thread is the only one that waits for operands, tiles
+  // and the outputs.  The copying thread waits for done_pw (SAVE: done_up) of every chunk
+  // and signals free_copy behind it, which the next chunk's last product waits for; what
+  // has one stage it copies behind the product (for v: the operand) that frees it, which
+  // cannot come round again before the copy.  The vectors come round every third chunk.
 
-  if (tid >= kLaneThreads) {
-    // ================================================================ outputs, copies
-    const bool copier = tid == kLaneThreads;
-    const long long kq_head = KDA ? h : h / (p.H / p.HK), kq_heads = KDA ? p.H : p.HK;
-    constexpr int KQB = kq_bytes(FORM, DK, TWO);
-    auto tri = [&](int c) { return p.tri + ((long long)(sr.slot0 + c) * p.H + h) * kTriBytes; };
-    auto copy = [&](void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-      mbar_arrive_expect_tx(bar, bytes);
-      bulk_g2s(dst, src, bytes, bar);
-    };
-    auto copy_kq = [&](int c) {
-      if (c >= nch) return;
-      copy(sm.st[c % NST].kq, p.kq + ((sr.slot0 + c) * kq_heads + kq_head) * KQB, Sm::KQ, &sm.full_kq[c % NST]);
-    };
-    auto copy_ke = [&](int c) {
-      if (!KDA || c >= nch) return;
-      copy(sm.st[c % NST].ke, p.kq + ((sr.slot0 + c) * kq_heads + kq_head) * KQB + 2 * TERM, TERM, &sm.full_ke[c % NST]);
-    };
-    auto copy_t = [&](int c) {
-      if (M2 || c >= nch) return;
-      copy(sm.st[c % NST].T, tri(c), 16384, &sm.full_t[c % NST]);
-    };
-    auto copy_p = [&](int c) {
-      if (SAVE || c >= nch) return;
-      copy(sm.st[c % NST].P, tri(c) + 16384, 16384, &sm.full_p[c % NST]);
-    };
-    auto copy_vec = [&](int c) {
-      if (c >= nch) return;
-      copy(&sm.vec[c % 3], tri(c) + kTriVec, kVecBytes, &sm.full_vec[c % 3]);
-    };
-    if (copier) {
-      for (int c = 0; c < 2; ++c) {
-        copy_vec(c);
-        if (c < NST) {
-          copy_kq(c);
-          copy_t(c);
-          copy_ke(c);
-          copy_p(c);
+  if (warp >= 12) {
+    // ================================================================ products, copies
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRestRegs));
+    if (warp == 12 && lane == 0) {
+      constexpr uint32_t kIdesc64 = umma_idesc(128, 64, false), kIdesc128 = umma_idesc(128, 128, false);
+      constexpr uint32_t kIdescUp = umma_idesc(128, DK, true);
+      constexpr int ROWS = KDA ? kChunk : 2 * kChunk;    // of the tile with the update's k
+      const auto step_kq = [](int ks) { return (uint32_t)((ks >> 2) * 16384 + (ks & 3) * 32); };
+      const auto step_sq = [](int ks) { return (uint32_t)(ks * 32); };
+      const auto step_up = [](int ks) { return (uint32_t)(ks * 2048); };
+      for (int c = 0; c < nch; ++c) {
+        const int kst = c % NKQ, kph = c / NKQ, tst = c % NTP, tph = c / NTP;
+        if constexpr (!(M2 && SAVE)) {
+          wait(&sm.full_kq[kst], kph);
+          if (!SAVE && c > 0) wait(&sm.free_q, c - 1);
+          wait(&sm.op_s, c);
+          tmem_fence_after();
+          const uint64_t tile = umma_desc(smem_addr(sm.kq[kst]), 16);
+          if constexpr (SAVE)
+            product<DK / 16, TWO, kIdesc64>(tm + kKQ, tm + kS, 64, tile, TERM, false, step_kq);
+          else if constexpr (M2)
+            product<DK / 16, TWO, kIdesc64>(tm + kKQ + 64, tm + kS, 64, tile + (8192 >> 4), TERM, false, step_kq);
+          else
+            product<DK / 16, TWO, kIdesc128>(tm + kKQ, tm + kS, 64, tile, TERM, false, step_kq);
+          umma_commit(&sm.done_kq);
+        }
+        if constexpr (!M2) {
+          wait(&sm.full_t[tst], tph);
+          wait(&sm.op_r, c);
+          tmem_fence_after();
+          product<4, true, kIdesc64>(tm + kKQ, tm + kRW, 32, umma_desc(smem_addr(sm.tt[tst]), 16), 8192, false, step_sq);
+          umma_commit(&sm.done_t);
+        }
+        if constexpr (KDA) wait(&sm.full_ke, c);
+        if constexpr (M2 && SAVE) wait(&sm.full_kq[kst], kph);
+        if (SAVE && c > 0) wait(&sm.free_copy, c - 1);
+        wait(&sm.op_e, c);
+        tmem_fence_after();
+        if constexpr (KDA)
+          product<4, true, kIdescUp>(tm + kUp, tm + kS, 32, umma_desc(smem_addr(sm.ke), ROWS * 128), TERM / 2, false, step_up);
+        else
+          product<4, TWO, kIdescUp>(tm + kUp, tm + kS, 32, umma_desc(smem_addr(sm.kq[kst]), ROWS * 128), TERM, false, step_up);
+        umma_commit(&sm.done_up);
+        if constexpr (!SAVE) {
+          wait(&sm.full_p[tst], tph);
+          if (c > 0) {
+            wait(&sm.free_pw, c - 1);
+            wait(&sm.free_copy, c - 1);
+          }
+          wait(&sm.op_w, c);
+          tmem_fence_after();
+          product<4, true, kIdesc64>(tm + kPW, tm + kRW, 32, umma_desc(smem_addr(sm.pp[tst]), 16), 8192, false, step_sq);
+          umma_commit(&sm.done_pw);
         }
       }
+    } else if (warp == 13 && lane == 0) {
+      const long long kq_head = KDA ? h : h / (p.H / p.HK), kq_heads = KDA ? p.H : p.HK;
+      constexpr int KQB = kq_bytes(FORM, DK, TWO);
+      auto tri = [&](int c) { return p.tri + ((long long)(sr.slot0 + c) * p.H + h) * kTriBytes; };
+      auto kq = [&](int c) { return p.kq + ((sr.slot0 + c) * kq_heads + kq_head) * KQB; };
+      auto copy = [&](void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+        mbar_arrive_expect_tx(bar, bytes);
+        bulk_g2s(dst, src, bytes, bar);
+      };
+      auto copy_kq = [&](int c) {
+        if (c < nch) copy(sm.kq[c % NKQ], kq(c), Sm::KQ, &sm.full_kq[c % NKQ]);
+      };
+      auto copy_ke = [&](int c) {
+        if (KDA && c < nch) copy(sm.ke, kq(c) + 2 * TERM, TERM, &sm.full_ke);
+      };
+      auto copy_t = [&](int c) {
+        if (!M2 && c < nch) copy(sm.tt[c % NTP], tri(c), 16384, &sm.full_t[c % NTP]);
+      };
+      auto copy_p = [&](int c) {
+        if (!SAVE && c < nch) copy(sm.pp[c % NTP], tri(c) + 16384, 16384, &sm.full_p[c % NTP]);
+      };
+      auto copy_vec = [&](int c) {
+        if (c < nch) copy(&sm.vec[c % 3], tri(c) + kTriVec, kVecBytes, &sm.full_vec[c % 3]);
+      };
+      auto copy_v = [&](int c) {      // the chunk's rows of v
+        if (c >= nch) return;
+        const int n = min(kChunk, sr.len - c * kChunk);
+        const T* src = static_cast<const T*>(p.v) + ((sr.first + (long long)c * kChunk) * p.H + h) * DV;
+        mbar_arrive_expect_tx(&sm.full_v, n * DV * (int)sizeof(T));
+#pragma unroll 4
+        for (int i = 0; i < n; ++i, src += vstep) bulk_g2s(sm.v + i * DV, src, DV * sizeof(T), &sm.full_v);
+      };
+      for (int c = 0; c < 2; ++c) {
+        copy_vec(c);
+        if (c < NKQ) copy_kq(c);
+        if (c == 0) copy_v(c);
+        if (c < NTP) copy_t(c);
+        if (c == 0) copy_ke(c);
+        if (c < NTP) copy_p(c);
+      }
+      for (int c = 0; c < nch; ++c) {
+        if constexpr (NKQ == 1) {
+          wait(&sm.done_kq, c);
+          copy_kq(c + 1);
+        }
+        wait(M2 ? &sm.op_e : &sm.op_r, c);
+        copy_v(c + 1);
+        if constexpr (NTP == 1 && !M2) {
+          wait(&sm.done_t, c);
+          copy_t(c + 1);
+        }
+        if constexpr (KDA) {
+          wait(&sm.done_up, c);
+          copy_ke(c + 1);
+        }
+        wait(SAVE ? &sm.done_up : &sm.done_pw, c);
+        if constexpr (NKQ == 2) copy_kq(c + 2);
+        if constexpr (NTP == 2) copy_t(c + 2);
+        copy_p(c + NTP);
+        copy_vec(c + 2);
+        mbar_arrive(&sm.free_copy);
+      }
+      if (sm.dead) {      // a wait ran out: let the copies in flight land all the same
+        const int c = nch - 1;
+        mbar_wait_bounded(&sm.full_kq[c % NKQ], (uint32_t)(c / NKQ) & 1u, kWaitLimitNs);
+        mbar_wait_bounded(&sm.full_v, (uint32_t)c & 1u, kWaitLimitNs);
+        mbar_wait_bounded(&sm.full_vec[c % 3], (uint32_t)(c / 3) & 1u, kWaitLimitNs);
+      }
     }
+  } else if (warp >= 8) {
+    // ================================================================ outputs
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kOutRegs));
     float nan = 0.f, top = 0.f;      // NaN once a result was not finite; the largest |o|
-    for (int c = 0; c < nch; ++c) {
+    for (int c = 0; !SAVE && c < nch; ++c) {
       const float(*vec)[kChunk] = sm.vec[c % 3].v;
       float o[kChunk];
-      if constexpr (!SAVE) {
+      {
         const int n = min(kChunk, sr.len - c * kChunk);
         wait(&sm.done_kq, c);
         wait(&sm.full_vec[c % 3], c / 3);
@@ -214,15 +327,7 @@ __global__ void __launch_bounds__(kPassThreads, 1) scan_pass_kernel(const ScanPa
         tmem_wait_ld();
         tmem_fence_before();
         const float invS = sm.inv[c & 1][0][j];
-        mbar_arrive(&sm.free_q);
-        if (NST == 1 && copier) {
-          copy_kq(c + 1);
-          wait(&sm.done_t, c);
-          copy_t(c + 1);
-          wait(&sm.done_up, c);
-          copy_ke(c + 1);
-        }
-        __syncwarp();
+        warp_arrive(&sm.free_q);
 #pragma unroll
         for (int x = 0; x < kChunk; x += 4) {
           const float4 f = ld4(&vec[kVecQ][x]);
@@ -249,60 +354,43 @@ __global__ void __launch_bounds__(kPassThreads, 1) scan_pass_kernel(const ScanPa
           }
         }
         tmem_fence_before();
-        mbar_arrive(&sm.free_pw);
-        if (copier) {
-          if (NST == 2) {
-            copy_kq(c + 2);
-            copy_t(c + 2);
-          }
-          copy_p(c + NST);
-          copy_vec(c + 2);
-        }
-        __syncwarp();
+        warp_arrive(&sm.free_pw);
         if (on) {
 #pragma unroll
           for (int e = 0; e < kChunk; ++e) {      // (tokens behind the chunk's have rows of zeros)
             nan = fmaf(o[e], 0.f, nan);
             top = fmaxf(top, fabsf(o[e]));
           }
-          T* dst = static_cast<T*>(p.o) + ((sr.first + (long long)c * kChunk) * p.H + h) * DV + j;
+        }
+        // through shared memory, so that whole rows go out in one copy each (a store per
+        // value and token would hold the load-store units for longer than the chunk takes)
+        const int ot = tid - kLaneThreads;
 #pragma unroll
-          for (int x = 0; x < kChunk; x += 16)
-            act_st_rows(dst + x * vstep, vstep, n - x, *reinterpret_cast<const float(*)[16]>(o + x));
-        }
-      } else {
-        if (NST == 1 && copier) {
-          wait(&sm.done_kq, c);
-          copy_kq(c + 1);
-          wait(&sm.done_t, c);
-          copy_t(c + 1);
-        }
-        wait(&sm.done_up, c);
-        if (copier) {
-          if (NST == 2) {
-            copy_kq(c + 2);
-            copy_t(c + 2);
-          } else {
-            copy_ke(c + 1);
+        for (int x = 0; x < kChunk; x += Sm::OROWS) {
+          if (ot < Sm::OROWS) bulk_wait_read();
+          named_sync(3, kOutThreads);
+          if (on) {
+#pragma unroll
+            for (int e = 0; e < Sm::OROWS; ++e) sm.o[e * DV + j] = fac_from_f<T>(o[x + e]);
           }
-          copy_vec(c + 2);
+          fence_proxy_async_smem();
+          named_sync(3, kOutThreads);
+          if (ot < Sm::OROWS && x + ot < n) {
+            bulk_s2g(static_cast<T*>(p.o) + ((sr.first + (long long)c * kChunk + x + ot) * p.H + h) * DV, sm.o + ot * DV,
+                     DV * sizeof(T));
+            bulk_commit();
+          }
         }
-        __syncwarp();
-        mbar_arrive(&sm.free_pw);
       }
     }
+    bulk_wait_read();
     if (!SAVE && (!(nan == 0.f) || !act_finite(top, p.elem))) raise_flag(p.status, SEED_FLAG_NONFINITE);
-    if (copier && sm.dead) {      // a wait ran out: let the copies in flight land all the same
-      const int c = nch - 1;
-      mbar_wait_bounded(&sm.full_kq[c % NST], (uint32_t)(c / NST) & 1u, kWaitLimitNs);
-      mbar_wait_bounded(&sm.full_vec[c % 3], (uint32_t)(c / 3) & 1u, kWaitLimitNs);
-    }
   } else {
     // ================================================================ lanes
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kLaneRegs));
     const int half = warp >> 2;
     constexpr int NS = DK / 2;                         // state columns per thread
     const int cs0 = half * NS, t0 = half * 32;         // its first state column, its first token
-    auto lane_sync = [&] { named_sync(2, kLaneThreads); };
     // the larger of both warps' values for these lanes
     auto pair_max = [&](int which, float a, float b) {
       float2* mx = sm.mx[which] + j;
@@ -313,67 +401,59 @@ __global__ void __launch_bounds__(kPassThreads, 1) scan_pass_kernel(const ScanPa
     };
     // 32 values in registers as an A operand at `at` (second term 32 columns behind)
     auto put_rw = [&](uint32_t at, const float (&x)[32], float s) {
-      uint32_t hi[16], lo[16];
 #pragma unroll
-      for (int e = 0; e < 16; ++e) split2(s * x[2 * e], s * x[2 * e + 1], hi[e], lo[e]);
-      tmem_st16(lanes + at + t0 / 2, hi);
-      tmem_st16(lanes + at + 32 + t0 / 2, lo);
+      for (int g = 0; g < 32; g += 16) {
+        uint32_t hi[8], lo[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) split2(s * x[g + 2 * e], s * x[g + 2 * e + 1], hi[e], lo[e]);
+        tmem_st8(lanes + at + (t0 + g) / 2, hi);
+        tmem_st8(lanes + at + 32 + (t0 + g) / 2, lo);
+      }
     };
-    auto handed = [&] {      // operands stored: before the barrier behind which they are used
+    auto hand = [&](uint64_t* op) {      // an operand is stored, everything read before it is read
       tmem_wait_st();
       tmem_fence_before();
-      lane_sync();
+      warp_arrive(op);
     };
-    constexpr uint32_t kIdesc64 = umma_idesc(128, 64, false), kIdesc128 = umma_idesc(128, 128, false);
-    constexpr uint32_t kIdescUp = umma_idesc(128, DK, true);
-    constexpr int ROWS = KDA ? kChunk : 2 * kChunk;    // of the tile with the update's k
     float S[NS];
 #pragma unroll
     for (int c = 0; c < NS; ++c) S[c] = on && p.S0 != nullptr ? p.S0[sh * mat + (long long)(cs0 + c) * DV + j] : 0.f;
     float invS = 1.f;
 
     for (int c = 0; c < nch; ++c) {
-      const int stg = c % NST, ph = c / NST;
       const long long first = sr.first + (long long)c * kChunk;
       const int n = min(kChunk, sr.len - c * kChunk);
-      typename Sm::Stage& st = sm.st[stg];
       const typename Sm::Vec& vc = sm.vec[c % 3];
       // ---- S^T as an operand, S^T (B k)^T and S^T (B q)^T
       if constexpr (!(M2 && SAVE)) {
-        float m = 0.f;
+        float m[4] = {};
 #pragma unroll
-        for (int x = 0; x < NS; ++x) m = fmaxf(m, fabsf(S[x]));
-        const float sS = pow2_scale(pair_max(0, m, 0.f).x);
+        for (int x = 0; x < NS; ++x) m[x & 3] = fmaxf(m[x & 3], fabsf(S[x]));
+        const float sS = pow2_scale(pair_max(0, fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])), 0.f).x);
         invS = pow2_inverse(sS);
         if (!SAVE && half == 0) sm.inv[c & 1][0][j] = invS;
 #pragma unroll
-        for (int x = 0; x < NS / 32; ++x) {
-          uint32_t hi[16], lo[16];
+        for (int x = 0; x < NS; x += 16) {
+          uint32_t hi[8], lo[8];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) split2(sS * S[32 * x + 2 * e], sS * S[32 * x + 2 * e + 1], hi[e], lo[e]);
-          tmem_st16(lanes + kS + cs0 / 2 + 16 * x, hi);
-          tmem_st16(lanes + kS + 64 + cs0 / 2 + 16 * x, lo);
+          for (int e = 0; e < 8; ++e) split2(sS * S[x + 2 * e], sS * S[x + 2 * e + 1], hi[e], lo[e]);
+          tmem_st8(lanes + kS + (cs0 + x) / 2, hi);
+          tmem_st8(lanes + kS + 64 + (cs0 + x) / 2, lo);
         }
-        handed();
-        if (tid == 0) {
-          tmem_fence_after();
-          wait(&sm.full_kq[stg], ph);
-          if (!SAVE && c > 0) wait(&sm.free_q, c - 1);
-          const auto step = [](int ks) { return (uint32_t)((ks >> 2) * 16384 + (ks & 3) * 32); };
-          const uint64_t tile = umma_desc(smem_addr(st.kq), 16);
-          if constexpr (SAVE)
-            product<DK / 16, TWO, kIdesc64>(tm + kKQ, tm + kS, 64, tile, TERM, false, step);
-          else if constexpr (M2)
-            product<DK / 16, TWO, kIdesc64>(tm + kKQ + 64, tm + kS, 64, tile + (8192 >> 4), TERM, false, step);
-          else
-            product<DK / 16, TWO, kIdesc128>(tm + kKQ, tm + kS, 64, tile, TERM, false, step);
-          umma_commit(&sm.done_kq);
-        }
-        __syncwarp();
+        hand(&sm.op_s);
       }
       // ---- r, w
       float x[32];
-      act_ld_rows(static_cast<const T*>(p.v) + ((first + t0) * p.H + h) * DV + j, vstep, on ? n - t0 : 0, x);
+      wait(&sm.full_v, c);
+      {
+        const T* src = sm.v + t0 * DV + j;
+        const int left = on ? n - t0 : 0;      // (rows behind the tokens hold an earlier chunk's)
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          const float y = fac_to_f(src[e * DV]);
+          x[e] = e < left ? y : 0.f;
+        }
+      }
       if constexpr (SAVE) {
         if (on) {
           float* dst = p.chunk_S + ((long long)(sr.slot0 + c) * p.H + h) * mat + (long long)cs0 * DV + j;
@@ -404,15 +484,7 @@ __global__ void __launch_bounds__(kPassThreads, 1) scan_pass_kernel(const ScanPa
         for (int e = 0; e < 32; ++e) m = fmaxf(m, fabsf(x[e]));
         const float sR = pow2_scale(pair_max(1, m, 0.f).x), invR = pow2_inverse(sR);
         put_rw(kRW, x, sR);
-        handed();
-        if (tid == 0) {
-          tmem_fence_after();
-          wait(&sm.full_t[stg], ph);
-          product<4, true, kIdesc64>(tm + kKQ, tm + kRW, 32, umma_desc(smem_addr(st.T), 16), 8192, false,
-                                     [](int ks) { return (uint32_t)(ks * 32); });
-          umma_commit(&sm.done_t);
-        }
-        __syncwarp();
+        hand(&sm.op_r);
         wait(&sm.done_t, c);
         tmem_fence_after();
         tmem_ld16(lanes + kKQ + t0, x);
@@ -439,53 +511,34 @@ __global__ void __launch_bounds__(kPassThreads, 1) scan_pass_kernel(const ScanPa
         if constexpr (!SAVE) wait(&sm.done_kq, c);
       }
       // ---- the state's update: E w times the k rows
-      float y[32];
       m = 0.f;
 #pragma unroll
       for (int e = 0; e < 32; e += 4) {
         const float4 fe = ld4(&vc.v[kVecE][t0 + e]);
-        y[e] = x[e] * fe.x;
-        y[e + 1] = x[e + 1] * fe.y;
-        y[e + 2] = x[e + 2] * fe.z;
-        y[e + 3] = x[e + 3] * fe.w;
-      }
-#pragma unroll
-      for (int e = 0; e < 32; ++e) {
-        m = fmaxf(m, fabsf(x[e]));
-        me = fmaxf(me, fabsf(y[e]));
+        m = fmaxf(fmaxf(fmaxf(m, fabsf(x[e])), fmaxf(fabsf(x[e + 1]), fabsf(x[e + 2]))), fabsf(x[e + 3]));
+        me = fmaxf(fmaxf(fmaxf(me, fabsf(x[e] * fe.x)), fmaxf(fabsf(x[e + 1] * fe.y), fabsf(x[e + 2] * fe.z))),
+                   fabsf(x[e + 3] * fe.w));
       }
       const float2 mm = pair_max(2, m, me);
       const float sW = pow2_scale(mm.x), sE = pow2_scale(mm.y), invE = pow2_inverse(sE);
-      put_rw(kS, y, sE);
-      if (!SAVE && half == 0) sm.inv[c & 1][1][j] = pow2_inverse(sW);
-      handed();
-      if (tid == 0) {
-        tmem_fence_after();
-        if (SAVE && c > 0) wait(&sm.free_pw, c - 1);
-        const auto step = [](int ks) { return (uint32_t)(ks * 2048); };
-        if constexpr (KDA) {
-          wait(&sm.full_ke[stg], ph);
-          product<4, true, kIdescUp>(tm + kUp, tm + kS, 32, umma_desc(smem_addr(st.ke), ROWS * 128), TERM / 2, false, step);
-        } else {
-          if constexpr (M2 && SAVE) wait(&sm.full_kq[stg], ph);
-          product<4, TWO, kIdescUp>(tm + kUp, tm + kS, 32, umma_desc(smem_addr(st.kq), ROWS * 128), TERM, false, step);
+#pragma unroll
+      for (int g = 0; g < 32; g += 16) {
+        uint32_t hi[8], lo[8];
+#pragma unroll
+        for (int e = 0; e < 16; e += 4) {
+          const float4 fe = ld4(&vc.v[kVecE][t0 + g + e]);
+          split2(sE * (x[g + e] * fe.x), sE * (x[g + e + 1] * fe.y), hi[e / 2], lo[e / 2]);
+          split2(sE * (x[g + e + 2] * fe.z), sE * (x[g + e + 3] * fe.w), hi[e / 2 + 1], lo[e / 2 + 1]);
         }
-        umma_commit(&sm.done_up);
+        tmem_st8(lanes + kS + (t0 + g) / 2, hi);
+        tmem_st8(lanes + kS + 32 + (t0 + g) / 2, lo);
       }
-      __syncwarp();
+      if (!SAVE && half == 0) sm.inv[c & 1][1][j] = pow2_inverse(sW);
+      hand(&sm.op_e);
       // ---- w P^T for the outputs, beside it
       if constexpr (!SAVE) {
         put_rw(kRW, x, sW);
-        handed();
-        if (tid == 0) {
-          tmem_fence_after();
-          wait(&sm.full_p[stg], ph);
-          if (c > 0) wait(&sm.free_pw, c - 1);
-          product<4, true, kIdesc64>(tm + kPW, tm + kRW, 32, umma_desc(smem_addr(st.P), 16), 8192, false,
-                                     [](int ks) { return (uint32_t)(ks * 32); });
-          umma_commit(&sm.done_pw);
-        }
-        __syncwarp();
+        hand(&sm.op_w);
       } else {
         act_st_rows(p.w + ((first + t0) * p.H + h) * DV + j, vstep, on ? n - t0 : 0, x);
       }
@@ -527,7 +580,7 @@ template <int FORM, int DK, int DV, typename T, bool SAVE>
 int launch_pass_t(const ScanParams& p, cudaStream_t st) {
   static LaunchCache cache;
   // one block per SM (it holds all of the SM's tensor memory)
-  constexpr size_t need = sizeof(PassSmem<FORM, DK, scan_two_terms(FORM, std::is_same<T, float>::value)>) + 1024;
+  constexpr size_t need = sizeof(PassSmem<FORM, DK, DV, T>) + 1024;
   constexpr size_t bytes = need < 116 * 1024 ? 116 * 1024 : need;
   static_assert(bytes <= 227 * 1024, "shared memory");
   int dev;

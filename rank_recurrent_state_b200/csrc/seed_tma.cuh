@@ -44,6 +44,16 @@ SEED_DEV void bulk_g2s(void* dst, const void* src, uint32_t bytes, uint64_t* bar
       : "memory");
 }
 
+// shared -> global bulk copy in this thread's bulk group; addresses and size as above.
+// The writer of the shared data orders it with fence_proxy_async_smem first.
+SEED_DEV void bulk_s2g(void* dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_addr(src)), "r"(bytes)
+               : "memory");
+}
+SEED_DEV void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+// Until this thread's bulk copies have read their shared-memory source.
+SEED_DEV void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+
 // Ampere-style asynchronous 16-byte copy global -> shared (no mbarrier): groups
 // are committed in order and waited for by count; each thread waits for its own.
 SEED_DEV void cp_async16(void* dst, const void* src) {
