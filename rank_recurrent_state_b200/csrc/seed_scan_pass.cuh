@@ -80,17 +80,21 @@ struct PassSmem {
 };
 static_assert(kVecBytes == sizeof(float) * (kVecs * kChunk + 128), "one layout");
 
-// Bounded wait; after the block's first failure every wait returns at once.
+// Bounded wait; after the block's first failure every wait returns at once.  The clock is
+// read on one try in 64: a try suspends the warp, but what stands between two of them takes
+// issue slots from the warps at work.
 SEED_DEV void pass_wait(uint64_t* bar, uint32_t phase, volatile int* dead, uint32_t* status) {
-  if (mbar_test_wait(bar, phase)) return;
-  if (*dead) return;
-  const uint64_t t0 = global_ns();
-  while (!mbar_try_wait(bar, phase)) {
-    if (*dead) return;
-    if (global_ns() - t0 > kWaitLimitNs) {
-      *dead = 1;
-      raise_flag(status, SEED_FLAG_TIMEOUT);
-      return;
+  uint64_t t0 = 0;
+  for (int i = 1; !mbar_try_wait_for(bar, phase, 1000000u); ++i) {
+    if ((i & 63) == 0) {
+      if (*dead) return;
+      const uint64_t t = global_ns();
+      if (t0 == 0) t0 = t;
+      if (t - t0 > kWaitLimitNs) {
+        *dead = 1;
+        raise_flag(status, SEED_FLAG_TIMEOUT);
+        return;
+      }
     }
   }
 }
@@ -313,7 +317,7 @@ __global__ void __launch_bounds__(kPassThreads, 1) scan_pass_kernel(const ScanPa
   } else if (warp >= 8) {
     // ================================================================ outputs
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kOutRegs));
-    float nan = 0.f, top = 0.f;      // NaN once a result was not finite; the largest |o|
+    float nan = 0.f;      // NaN once a stored result was not finite
     for (int c = 0; !SAVE && c < nch; ++c) {
       const float(*vec)[kChunk] = sm.vec[c % 3].v;
       float o[kChunk];
@@ -355,13 +359,6 @@ __global__ void __launch_bounds__(kPassThreads, 1) scan_pass_kernel(const ScanPa
         }
         tmem_fence_before();
         warp_arrive(&sm.free_pw);
-        if (on) {
-#pragma unroll
-          for (int e = 0; e < kChunk; ++e) {      // (tokens behind the chunk's have rows of zeros)
-            nan = fmaf(o[e], 0.f, nan);
-            top = fmaxf(top, fabsf(o[e]));
-          }
-        }
         // through shared memory, so that whole rows go out in one copy each (a store per
         // value and token would hold the load-store units for longer than the chunk takes)
         const int ot = tid - kLaneThreads;
@@ -371,7 +368,11 @@ __global__ void __launch_bounds__(kPassThreads, 1) scan_pass_kernel(const ScanPa
           named_sync(3, kOutThreads);
           if (on) {
 #pragma unroll
-            for (int e = 0; e < Sm::OROWS; ++e) sm.o[e * DV + j] = fac_from_f<T>(o[x + e]);
+            for (int e = 0; e < Sm::OROWS; ++e) {      // (tokens behind the chunk's have rows of zeros)
+              const T t = fac_from_f<T>(o[x + e]);
+              sm.o[e * DV + j] = t;
+              nan = fmaf(fac_to_f(t), 0.f, nan);
+            }
           }
           fence_proxy_async_smem();
           named_sync(3, kOutThreads);
@@ -384,7 +385,7 @@ __global__ void __launch_bounds__(kPassThreads, 1) scan_pass_kernel(const ScanPa
       }
     }
     bulk_wait_read();
-    if (!SAVE && (!(nan == 0.f) || !act_finite(top, p.elem))) raise_flag(p.status, SEED_FLAG_NONFINITE);
+    if (!(nan == 0.f)) raise_flag(p.status, SEED_FLAG_NONFINITE);
   } else {
     // ================================================================ lanes
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kLaneRegs));
@@ -405,7 +406,7 @@ __global__ void __launch_bounds__(kPassThreads, 1) scan_pass_kernel(const ScanPa
       for (int g = 0; g < 32; g += 16) {
         uint32_t hi[8], lo[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) split2(s * x[g + 2 * e], s * x[g + 2 * e + 1], hi[e], lo[e]);
+        for (int e = 0; e < 8; ++e) split2_scaled(x[g + 2 * e], x[g + 2 * e + 1], s, hi[e], lo[e]);
         tmem_st8(lanes + at + (t0 + g) / 2, hi);
         tmem_st8(lanes + at + 32 + (t0 + g) / 2, lo);
       }
@@ -436,7 +437,7 @@ __global__ void __launch_bounds__(kPassThreads, 1) scan_pass_kernel(const ScanPa
         for (int x = 0; x < NS; x += 16) {
           uint32_t hi[8], lo[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) split2(sS * S[x + 2 * e], sS * S[x + 2 * e + 1], hi[e], lo[e]);
+          for (int e = 0; e < 8; ++e) split2_scaled(S[x + 2 * e], S[x + 2 * e + 1], sS, hi[e], lo[e]);
           tmem_st8(lanes + kS + (cs0 + x) / 2, hi);
           tmem_st8(lanes + kS + 64 + (cs0 + x) / 2, lo);
         }
@@ -527,8 +528,10 @@ __global__ void __launch_bounds__(kPassThreads, 1) scan_pass_kernel(const ScanPa
 #pragma unroll
         for (int e = 0; e < 16; e += 4) {
           const float4 fe = ld4(&vc.v[kVecE][t0 + g + e]);
-          split2(sE * (x[g + e] * fe.x), sE * (x[g + e + 1] * fe.y), hi[e / 2], lo[e / 2]);
-          split2(sE * (x[g + e + 2] * fe.z), sE * (x[g + e + 3] * fe.w), hi[e / 2 + 1], lo[e / 2 + 1]);
+          const float2 a = mul2(mul2(make_float2(x[g + e], x[g + e + 1]), make_float2(fe.x, fe.y)), sE);
+          const float2 b = mul2(mul2(make_float2(x[g + e + 2], x[g + e + 3]), make_float2(fe.z, fe.w)), sE);
+          split2(a.x, a.y, hi[e / 2], lo[e / 2]);
+          split2(b.x, b.y, hi[e / 2 + 1], lo[e / 2 + 1]);
         }
         tmem_st8(lanes + kS + (t0 + g) / 2, hi);
         tmem_st8(lanes + kS + 32 + (t0 + g) / 2, lo);
@@ -552,7 +555,12 @@ __global__ void __launch_bounds__(kPassThreads, 1) scan_pass_kernel(const ScanPa
         tmem_ld16(lanes + kUp + cs0 + z, a);
         tmem_wait_ld();
 #pragma unroll
-        for (int e = 0; e < 16; ++e) S[z + e] = fmaf(a[e], invE, (KDA ? vc.end[cs0 + z + e] : end) * S[z + e]);
+        for (int e = 0; e < 16; e += 2) {
+          const float2 d = KDA ? *reinterpret_cast<const float2*>(&vc.end[cs0 + z + e]) : make_float2(end, end);
+          const float2 y = fma2(make_float2(a[e], a[e + 1]), make_float2(invE, invE), mul2(d, make_float2(S[z + e], S[z + e + 1])));
+          S[z + e] = y.x;
+          S[z + e + 1] = y.y;
+        }
       }
       tmem_fence_before();
     }

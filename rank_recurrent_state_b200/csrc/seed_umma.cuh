@@ -101,12 +101,39 @@ SEED_DEV float pow2_scale(float m) {
 }
 SEED_DEV float pow2_inverse(float s) { return __uint_as_float((254u << 23) - __float_as_uint(s)); }
 
+// Two float32 operations in one instruction.
+SEED_DEV uint64_t pack2(float2 a) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a.x), "f"(a.y));
+  return r;
+}
+SEED_DEV float2 unpack2(uint64_t a) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a));
+  return r;
+}
+SEED_DEV float2 mul2(float2 a, float2 b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pack2(a)), "l"(pack2(b)));
+  return unpack2(r);
+}
+SEED_DEV float2 mul2(float2 a, float b) { return mul2(a, make_float2(b, b)); }
+SEED_DEV float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(pack2(a)), "l"(pack2(b)), "l"(pack2(c)));
+  return unpack2(r);
+}
+
 SEED_DEV void split2(float x, float y, uint32_t& hi, uint32_t& lo) {
   const __half2 h = __floats2half2_rn(x, y);
-  const float2 f = __half22float2(h);
-  const __half2 l = __floats2half2_rn(x - f.x, y - f.y);
+  const float2 d = fma2(__half22float2(h), make_float2(-1.f, -1.f), make_float2(x, y));      // exact
+  const __half2 l = __floats2half2_rn(d.x, d.y);
   memcpy(&hi, &h, 4);
   memcpy(&lo, &l, 4);
+}
+SEED_DEV void split2_scaled(float x, float y, float s, uint32_t& hi, uint32_t& lo) {
+  const float2 a = mul2(make_float2(x, y), s);
+  split2(a.x, a.y, hi, lo);
 }
 
 }  // namespace seed
