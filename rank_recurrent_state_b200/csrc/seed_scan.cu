@@ -121,7 +121,12 @@ int launch_scan_backward(const seed_scan_dims& d, const int32_t* offsets, const 
   p.status = static_cast<uint32_t*>(ws);
   int rc;
   if ((rc = forward(p, d, st))) return rc;                        // w and the state before each chunk
-  if ((rc = launch_scan_step_back(p, d.form, st))) return rc;     // dw, the gradient behind each chunk, dS0
+  // dw, the gradient behind each chunk, dS0
+  if (chunked(p, d))
+    rc = with_factor_type_of(d.elem, [&](auto t) -> int { return launch_scan_back_as<decltype(t)>(p, d.form, st); });
+  else
+    rc = launch_scan_step_back(p, d.form, st);
+  if (rc) return rc;
   if (d.tokens == 0) return SEED_OK;
   if ((rc = launch_scan_grad(p, d.form, st))) return rc;
   return p.part ? launch_scan_share(p, st) : SEED_OK;

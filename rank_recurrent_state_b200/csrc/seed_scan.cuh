@@ -215,6 +215,9 @@ int launch_scan_prep_as(const ScanParams& p, int form, cudaStream_t st);
 // d_k and d_v in {64, 128}; writes w and chunk_S instead of o and S_out where chunk_S is set.
 template <typename T>
 int launch_scan_pass_as(const ScanParams& p, int form, cudaStream_t st);
+// The reverse recurrence on the tensor cores (seed_scan_back.cuh), behind launch_scan_prep_as.
+template <typename T>
+int launch_scan_back_as(const ScanParams& p, int form, cudaStream_t st);
 // Gradients of each chunk from its states (seed_scan_grad.cu).
 int launch_scan_grad(const ScanParams& p, int form, cudaStream_t st);
 // Sum of dq and dk over the heads that share a key head.
