@@ -18,7 +18,8 @@
 // One block per (chunk, head), all products in float32 FMA from shared memory; the
 // decays run as products along the chunk, so zeros and per-channel decays need no case
 // of their own.  Bound by FMA issue and shared-memory reads.
-#include "seed_scan.cuh"
+#include "seed_scan_pass.cuh"
+#include "seed_scan_prep.cuh"
 
 namespace seed {
 
@@ -50,157 +51,15 @@ struct GradSmem {
 template <int G>
 SEED_DEV float lanes_sum(float x) { return group_sum<G>(x); }
 
-template <int FORM, int DK, int DV>
-__global__ void __launch_bounds__(kNT, 1) scan_grad_kernel(const ScanParams p) {
+// The sums over the chunk, the outputs and the decays' gradients, from q, k, the state's
+// products (sm.out), X and Y (sm.xy) in shared memory.  E: (S0 dS^T)_cc in thread c < DK.
+template <int FORM, int DK, typename Sm>
+SEED_DEV void grad_sums(const ScanParams& p, const ChunkAt& ck, int h, Sm& sm, float E) {
   constexpr bool KDA = FORM == SEED_KDA, M2 = FORM == SEED_MAMBA2;
-  using Sm = GradSmem<DK, DV>;
-  constexpr int PK = Sm::PK, PV = Sm::PV, PT = Sm::PT, PX = Sm::PX, CT = Sm::CT;
-  extern __shared__ __align__(16) unsigned char smem_raw[];
-  Sm& sm = *reinterpret_cast<Sm*>(smem_raw);
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int slot = blockIdx.x / p.H, h = blockIdx.x - slot * p.H;
-  ChunkAt ck;
-  if (!chunk_at(p, slot, &ck)) return;
-  const int n = ck.n;
-  const int hk = h / (p.H / p.HK);
-  const long long mat = (long long)DK * DV;
-  const float* S0 = p.chunk_S + ((long long)slot * p.H + h) * mat;
-  const float* dS = p.chunk_dS + ((long long)slot * p.H + h) * mat;
+  constexpr int PK = Sm::PK, PX = Sm::PX;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int n = ck.n, hk = h / (p.H / p.HK);
   const float* al = p.alpha;
-
-  // ---- inputs; rows behind the chunk's tokens are zero
-  act_type(p.elem, [&](auto tag) {
-    using E = decltype(tag);
-#pragma unroll 4
-    for (int e = tid; e < kChunk * DK / 4; e += kNT) {
-      const int i = e / (DK / 4), c = 4 * (e % (DK / 4));
-      float4 a = zero4(), b = zero4();
-      if (i < n) {
-        const long long at = ((ck.first + i) * p.HK + hk) * DK + c;
-        a = fac_ld4(static_cast<const E*>(p.q) + at);
-        b = fac_ld4(static_cast<const E*>(p.k) + at);
-      }
-      st4(&sm.q[i * PK + c], a);
-      st4(&sm.k[i * PK + c], b);
-    }
-#pragma unroll 4
-    for (int e = tid; e < kChunk * DV / 4; e += kNT) {
-      const int i = e / (DV / 4), c = 4 * (e % (DV / 4));
-      float4 a = zero4(), b = zero4(), d = zero4();
-      if (i < n) {
-        const long long at = ((ck.first + i) * p.H + h) * DV + c;
-        a = fac_ld4(static_cast<const E*>(p.d_o) + at);
-        b = ld4(p.w + at);
-        d = ld4(p.dw + at);
-      }
-      st4(&sm.in.d_o[i * PV + c], a);
-      st4(&sm.in.w[i * PV + c], b);
-      st4(&sm.in.dw[i * PV + c], d);
-    }
-  });
-  if (tid < kChunk) {
-    sm.beta[tid] = tid < n ? p.beta[(ck.first + tid) * p.H + h] : 0.f;
-    if constexpr (!KDA) sm.alpha[tid] = tid < n ? al[(ck.first + tid) * p.H + h] : 1.f;
-  }
-  __syncthreads();
-
-  // ---- dv and v . dw, a warp per row
-  for (int i = warp; i < n; i += kNT / 32) {
-    const long long row = ((ck.first + i) * p.H + h) * DV;
-    float x = 0.f;
-    for (int c = lane; c < DV; c += 32) {
-      const float d = sm.in.dw[i * PV + c];
-      x = fmaf(act_ld(p.v, row + c, p.elem), d, x);
-      act_st(p.dv_, row + c, sm.beta[i] * d, p.elem);
-    }
-    x = group_sum<32>(x);
-    if (lane == 0) sm.kh[i] = x;
-  }
-
-  // ---- S0 do, S0 dw, dS w: thread tile of 4 rows x DK / 16 columns
-  constexpr int NC = DK / 16;
-  const int ty = tid >> 4, tx = tid & 15;
-  float aq[4][NC] = {}, ah[4][NC] = {}, ac[4][NC] = {};
-  float E = 0.f;         // thread c < DK: (S0 dS^T)_cc
-  for (int j0 = 0; j0 < DV; j0 += CT) {
-    __syncthreads();
-    for (int e = tid; e < DK * CT / 4; e += kNT) {
-      const int c = e / (CT / 4), jj = 4 * (e % (CT / 4));
-      st4(&sm.t.S0[c * PT + jj], ld4(S0 + (long long)c * DV + j0 + jj));
-      st4(&sm.t.dS[c * PT + jj], ld4(dS + (long long)c * DV + j0 + jj));
-    }
-    __syncthreads();
-    if (tid < DK) {
-#pragma unroll
-      for (int jj = 0; jj < CT; jj += 4) E += dot4(ld4(&sm.t.S0[tid * PT + jj]), ld4(&sm.t.dS[tid * PT + jj]));
-    }
-#pragma unroll
-    for (int jj = 0; jj < CT; jj += 4) {
-      float4 xo[4], xd[4], xw[4];
-#pragma unroll
-      for (int a = 0; a < 4; ++a) {
-        const int at = (ty + 16 * a) * PV + j0 + jj;
-        xo[a] = ld4(&sm.in.d_o[at]);
-        if constexpr (!M2) xd[a] = ld4(&sm.in.dw[at]);
-        xw[a] = ld4(&sm.in.w[at]);
-      }
-#pragma unroll
-      for (int b = 0; b < NC; ++b) {
-        const float4 s = ld4(&sm.t.S0[(tx + 16 * b) * PT + jj]);
-        const float4 g = ld4(&sm.t.dS[(tx + 16 * b) * PT + jj]);
-#pragma unroll
-        for (int a = 0; a < 4; ++a) {
-          aq[a][b] += dot4(xo[a], s);
-          if constexpr (!M2) ah[a][b] += dot4(xd[a], s);
-          ac[a][b] += dot4(xw[a], g);
-        }
-      }
-    }
-  }
-  __syncthreads();
-  // ---- X and Y, kept as [column j][row i] (a row block of four is one float4)
-  {
-    float X[4][4] = {}, Y[4][4] = {};
-    for (int jj = 0; jj < DV; jj += 4) {
-      float4 xo[4], xd[4];
-#pragma unroll
-      for (int a = 0; a < 4; ++a) {
-        xo[a] = ld4(&sm.in.d_o[(ty + 16 * a) * PV + jj]);
-        if constexpr (!M2) xd[a] = ld4(&sm.in.dw[(ty + 16 * a) * PV + jj]);
-      }
-#pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        const float4 w = ld4(&sm.in.w[(tx + 16 * b) * PV + jj]);
-#pragma unroll
-        for (int a = 0; a < 4; ++a) {
-          X[a][b] += dot4(xo[a], w);
-          if constexpr (!M2) Y[a][b] += dot4(xd[a], w);
-        }
-      }
-    }
-    // (the state tiles X and Y overlay were last read before the barrier above)
-#pragma unroll
-    for (int a = 0; a < 4; ++a)
-#pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        const int i = ty + 16 * a, j = tx + 16 * b;
-        sm.xy.X[j * PX + i] = j < i ? X[a][b] : 0.f;
-        if (i == j) sm.xd[i] = X[a][b];
-        if constexpr (!M2) sm.xy.Y[j * PX + i] = j < i ? Y[a][b] : 0.f;
-      }
-  }
-  __syncthreads();
-#pragma unroll
-  for (int a = 0; a < 4; ++a)
-#pragma unroll
-    for (int b = 0; b < NC; ++b) {
-      const int at = (ty + 16 * a) * PK + tx + 16 * b;
-      sm.out.dq[at] = aq[a][b];
-      if constexpr (!M2) sm.out.h[at] = ah[a][b];
-      sm.out.c[at] = ac[a][b];
-    }
-  __syncthreads();
-
   // ---- sums over the chunk: a thread owns channel c and every NG-th block of 4 rows
   constexpr int NG = kNT / DK;
   constexpr int LG = DK < 32 ? DK : 32;
@@ -380,6 +239,360 @@ __global__ void __launch_bounds__(kNT, 1) scan_grad_kernel(const ScanParams p) {
   }
 }
 
+template <int FORM, int DK, int DV>
+__global__ void __launch_bounds__(kNT, 1) scan_grad_kernel(const ScanParams p) {
+  constexpr bool KDA = FORM == SEED_KDA, M2 = FORM == SEED_MAMBA2;
+  using Sm = GradSmem<DK, DV>;
+  constexpr int PK = Sm::PK, PV = Sm::PV, PT = Sm::PT, PX = Sm::PX, CT = Sm::CT;
+  extern __shared__ __align__(16) unsigned char smem_raw[];
+  Sm& sm = *reinterpret_cast<Sm*>(smem_raw);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int slot = blockIdx.x / p.H, h = blockIdx.x - slot * p.H;
+  ChunkAt ck;
+  if (!chunk_at(p, slot, &ck)) return;
+  const int n = ck.n;
+  const int hk = h / (p.H / p.HK);
+  const long long mat = (long long)DK * DV;
+  const float* S0 = p.chunk_S + ((long long)slot * p.H + h) * mat;
+  const float* dS = p.chunk_dS + ((long long)slot * p.H + h) * mat;
+  const float* al = p.alpha;
+
+  // ---- inputs; rows behind the chunk's tokens are zero
+  act_type(p.elem, [&](auto tag) {
+    using E = decltype(tag);
+#pragma unroll 4
+    for (int e = tid; e < kChunk * DK / 4; e += kNT) {
+      const int i = e / (DK / 4), c = 4 * (e % (DK / 4));
+      float4 a = zero4(), b = zero4();
+      if (i < n) {
+        const long long at = ((ck.first + i) * p.HK + hk) * DK + c;
+        a = fac_ld4(static_cast<const E*>(p.q) + at);
+        b = fac_ld4(static_cast<const E*>(p.k) + at);
+      }
+      st4(&sm.q[i * PK + c], a);
+      st4(&sm.k[i * PK + c], b);
+    }
+#pragma unroll 4
+    for (int e = tid; e < kChunk * DV / 4; e += kNT) {
+      const int i = e / (DV / 4), c = 4 * (e % (DV / 4));
+      float4 a = zero4(), b = zero4(), d = zero4();
+      if (i < n) {
+        const long long at = ((ck.first + i) * p.H + h) * DV + c;
+        a = fac_ld4(static_cast<const E*>(p.d_o) + at);
+        b = ld4(p.w + at);
+        d = ld4(p.dw + at);
+      }
+      st4(&sm.in.d_o[i * PV + c], a);
+      st4(&sm.in.w[i * PV + c], b);
+      st4(&sm.in.dw[i * PV + c], d);
+    }
+  });
+  if (tid < kChunk) {
+    sm.beta[tid] = tid < n ? p.beta[(ck.first + tid) * p.H + h] : 0.f;
+    if constexpr (!KDA) sm.alpha[tid] = tid < n ? al[(ck.first + tid) * p.H + h] : 1.f;
+  }
+  __syncthreads();
+
+  // ---- dv and v . dw, a warp per row
+  for (int i = warp; i < n; i += kNT / 32) {
+    const long long row = ((ck.first + i) * p.H + h) * DV;
+    float x = 0.f;
+    for (int c = lane; c < DV; c += 32) {
+      const float d = sm.in.dw[i * PV + c];
+      x = fmaf(act_ld(p.v, row + c, p.elem), d, x);
+      act_st(p.dv_, row + c, sm.beta[i] * d, p.elem);
+    }
+    x = group_sum<32>(x);
+    if (lane == 0) sm.kh[i] = x;
+  }
+
+  // ---- S0 do, S0 dw, dS w: thread tile of 4 rows x DK / 16 columns
+  constexpr int NC = DK / 16;
+  const int ty = tid >> 4, tx = tid & 15;
+  float aq[4][NC] = {}, ah[4][NC] = {}, ac[4][NC] = {};
+  float E = 0.f;         // thread c < DK: (S0 dS^T)_cc
+  for (int j0 = 0; j0 < DV; j0 += CT) {
+    __syncthreads();
+    for (int e = tid; e < DK * CT / 4; e += kNT) {
+      const int c = e / (CT / 4), jj = 4 * (e % (CT / 4));
+      st4(&sm.t.S0[c * PT + jj], ld4(S0 + (long long)c * DV + j0 + jj));
+      st4(&sm.t.dS[c * PT + jj], ld4(dS + (long long)c * DV + j0 + jj));
+    }
+    __syncthreads();
+    if (tid < DK) {
+#pragma unroll
+      for (int jj = 0; jj < CT; jj += 4) E += dot4(ld4(&sm.t.S0[tid * PT + jj]), ld4(&sm.t.dS[tid * PT + jj]));
+    }
+#pragma unroll
+    for (int jj = 0; jj < CT; jj += 4) {
+      float4 xo[4], xd[4], xw[4];
+#pragma unroll
+      for (int a = 0; a < 4; ++a) {
+        const int at = (ty + 16 * a) * PV + j0 + jj;
+        xo[a] = ld4(&sm.in.d_o[at]);
+        if constexpr (!M2) xd[a] = ld4(&sm.in.dw[at]);
+        xw[a] = ld4(&sm.in.w[at]);
+      }
+#pragma unroll
+      for (int b = 0; b < NC; ++b) {
+        const float4 s = ld4(&sm.t.S0[(tx + 16 * b) * PT + jj]);
+        const float4 g = ld4(&sm.t.dS[(tx + 16 * b) * PT + jj]);
+#pragma unroll
+        for (int a = 0; a < 4; ++a) {
+          aq[a][b] += dot4(xo[a], s);
+          if constexpr (!M2) ah[a][b] += dot4(xd[a], s);
+          ac[a][b] += dot4(xw[a], g);
+        }
+      }
+    }
+  }
+  __syncthreads();
+  // ---- X and Y, kept as [column j][row i] (a row block of four is one float4)
+  {
+    float X[4][4] = {}, Y[4][4] = {};
+    for (int jj = 0; jj < DV; jj += 4) {
+      float4 xo[4], xd[4];
+#pragma unroll
+      for (int a = 0; a < 4; ++a) {
+        xo[a] = ld4(&sm.in.d_o[(ty + 16 * a) * PV + jj]);
+        if constexpr (!M2) xd[a] = ld4(&sm.in.dw[(ty + 16 * a) * PV + jj]);
+      }
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        const float4 w = ld4(&sm.in.w[(tx + 16 * b) * PV + jj]);
+#pragma unroll
+        for (int a = 0; a < 4; ++a) {
+          X[a][b] += dot4(xo[a], w);
+          if constexpr (!M2) Y[a][b] += dot4(xd[a], w);
+        }
+      }
+    }
+    // (the state tiles X and Y overlay were last read before the barrier above)
+#pragma unroll
+    for (int a = 0; a < 4; ++a)
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        const int i = ty + 16 * a, j = tx + 16 * b;
+        sm.xy.X[j * PX + i] = j < i ? X[a][b] : 0.f;
+        if (i == j) sm.xd[i] = X[a][b];
+        if constexpr (!M2) sm.xy.Y[j * PX + i] = j < i ? Y[a][b] : 0.f;
+      }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int a = 0; a < 4; ++a)
+#pragma unroll
+    for (int b = 0; b < NC; ++b) {
+      const int at = (ty + 16 * a) * PK + tx + 16 * b;
+      sm.out.dq[at] = aq[a][b];
+      if constexpr (!M2) sm.out.h[at] = ah[a][b];
+      sm.out.c[at] = ac[a][b];
+    }
+  __syncthreads();
+
+  grad_sums<FORM, DK>(p, ck, h, sm, E);
+}
+
+// The same with the products of the states, X and Y on the tensor cores (two-term fp16,
+// seed_umma.cuh), for d_k, d_v in {64, 128}.  Operands are row-scaled K-major tiles along
+// the value channels: OD = [do; dw], W = w, and S0, then dS in the same place:
+//     S0 OD^T (key channel x 128 tokens), OD W^T (X and Y), dS W^T (key channel x 64 tokens)
+// The results replace the tiles in shared memory; the sums over the chunk are as above.
+template <int DK, int DV>
+struct GradUmmaSmem {
+  static constexpr int PK = DK + 4, PX = kChunk + 4;
+  static constexpr int OD = DV * 256, W = DV * 128, SX = DV * 256;      // one term each
+  union {
+    struct {
+      alignas(1024) unsigned char od[2 * OD], w[2 * W], sx[2 * SX];
+    } tile;
+    struct {
+      alignas(1024) float q[kChunk * PK];
+      float k[kChunk * PK];
+      struct { float dq[kChunk * PK], h[kChunk * PK], c[kChunk * PK]; } out;
+      struct { float X[kChunk * PX], Y[kChunk * PX]; } xy;
+    };
+  };
+  float alpha[kChunk], beta[kChunk], kh[kChunk], xd[kChunk], val[8];
+  float E[kNT];
+  float red[8][kChunk][2];
+  float inv_od[128], inv_w[kChunk], inv_s[128], Epart[128];
+  uint64_t done[2];
+  uint32_t tmem;
+  int dead;
+};
+
+template <int FORM, int DK, int DV, typename T>
+__global__ void __launch_bounds__(kNT, 1) scan_grad_umma_kernel(const ScanParams p) {
+  constexpr bool KDA = FORM == SEED_KDA, M2 = FORM == SEED_MAMBA2;
+  using Sm = GradUmmaSmem<DK, DV>;
+  constexpr int PK = Sm::PK, PX = Sm::PX;
+  extern __shared__ unsigned char smem_raw[];
+  Sm& sm = *reinterpret_cast<Sm*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int slot = blockIdx.x / p.H, h = blockIdx.x - slot * p.H;
+  ChunkAt ck;
+  if (!chunk_at(p, slot, &ck)) return;
+  const int n = ck.n, hk = h / (p.H / p.HK);
+  const long long mat = (long long)DK * DV;
+  const float* S0 = p.chunk_S + ((long long)slot * p.H + h) * mat;
+  const float* dS = p.chunk_dS + ((long long)slot * p.H + h) * mat;
+  if (tid == 0) {
+    mbar_init(&sm.done[0], 1);
+    mbar_init(&sm.done[1], 1);
+    fence_mbar_init();
+    sm.dead = 0;
+  }
+  if (warp == 0) tmem_alloc(&sm.tmem, 256);
+
+  // ---- operand tiles; a thread holds eight value channels of every RPI-th row
+  constexpr int LPR = DV / 8, RPI = kNT / LPR, IT = kChunk / RPI;
+  const int r0 = tid / LPR, c0 = 8 * (tid % LPR);
+  const long long row = (ck.first + r0) * p.H + h, step = (long long)RPI * p.H;
+  const int left = (n - r0 + RPI - 1) / RPI;
+  if (tid < kChunk) {
+    sm.beta[tid] = tid < n ? p.beta[(ck.first + tid) * p.H + h] : 0.f;
+    if constexpr (!KDA) sm.alpha[tid] = tid < n ? p.alpha[(ck.first + tid) * p.H + h] : 1.f;
+  }
+  {
+    float a[IT][8], b[IT][8], v[IT][8];
+    act_ld8_rows(static_cast<const T*>(p.d_o) + row * DV + c0, step * DV, left, a);
+    act_ld8_rows(p.dw + row * DV + c0, step * DV, left, b);
+    act_ld8_rows(static_cast<const T*>(p.v) + row * DV + c0, step * DV, left, v);
+    tile_rows<true, LPR, RPI, IT>(sm.tile.od, Sm::OD, 128, 0, sm.inv_od, a, r0, c0, nullptr, 0);
+    tile_rows<true, LPR, RPI, IT>(sm.tile.od, Sm::OD, 128, kChunk, sm.inv_od + kChunk, b, r0, c0, nullptr, 0);
+    act_ld8_rows(p.w + row * DV + c0, step * DV, left, a);
+    tile_rows<true, LPR, RPI, IT>(sm.tile.w, Sm::W, kChunk, 0, sm.inv_w, a, r0, c0, nullptr, 0);
+    // dv and v . dw
+#pragma unroll
+    for (int it = 0; it < IT; ++it) {
+      const int i = r0 + it * RPI;
+      float x = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x = fmaf(v[it][e], b[it][e], x);
+#pragma unroll
+      for (int off = LPR / 2; off >= 1; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
+      if (c0 == 0) sm.kh[i] = x;
+      if (i < n) {
+        const float be = p.beta[(ck.first + i) * p.H + h];
+        const long long at = (row + it * step) * DV + c0;
+        act_st4(p.dv_, at, make_float4(be * b[it][0], be * b[it][1], be * b[it][2], be * b[it][3]), p.elem);
+        act_st4(p.dv_, at + 4, make_float4(be * b[it][4], be * b[it][5], be * b[it][6], be * b[it][7]), p.elem);
+      }
+    }
+  }
+  auto state_tile = [&](const float* M, bool second) {
+#pragma unroll 1
+    for (int x = 0; x < DK; x += kChunk) {
+      float a[IT][8], b[IT][8];
+      act_ld8_rows(M + (long long)(x + r0) * DV + c0, (long long)RPI * DV, IT, a);
+      if (second) {
+        act_ld8_rows(S0 + (long long)(x + r0) * DV + c0, (long long)RPI * DV, IT, b);
+#pragma unroll
+        for (int it = 0; it < IT; ++it) {
+          float e = 0.f;
+#pragma unroll
+          for (int y = 0; y < 8; ++y) e = fmaf(a[it][y], b[it][y], e);
+#pragma unroll
+          for (int off = LPR / 2; off >= 1; off >>= 1) e += __shfl_xor_sync(0xffffffffu, e, off);
+          if (c0 == 0) sm.Epart[x + r0 + it * RPI] = e;
+        }
+      }
+      tile_rows<true, LPR, RPI, IT>(sm.tile.sx, Sm::SX, 128, x, sm.inv_s + x, a, r0, c0, nullptr, 0);
+    }
+  };
+  state_tile(S0, false);
+  fence_proxy_async_smem();
+  tmem_fence_before();
+  __syncthreads();
+  tmem_fence_after();
+  const uint32_t tm = sm.tmem;
+  constexpr uint32_t kSO = 0, kXY = 128, kSW = 192;      // accumulators' columns
+  const auto step128 = [](int ks) { return (uint32_t)((ks >> 2) * 16384 + (ks & 3) * 32); };
+  const auto step64 = [](int ks) { return (uint32_t)((ks >> 2) * 8192 + (ks & 3) * 32); };
+  if (tid == 0) {
+    const uint64_t od = umma_desc(smem_addr(sm.tile.od), 16), w = umma_desc(smem_addr(sm.tile.w), 16);
+    const uint64_t sx = umma_desc(smem_addr(sm.tile.sx), 16);
+    product_ss<DV / 16, umma_idesc(128, M2 ? 64 : 128, false)>(tm + kSO, sx, Sm::SX, step128, od, Sm::OD, step128);
+    umma_commit(&sm.done[0]);
+    product_ss<DV / 16, umma_idesc(128, 64, false)>(tm + kXY, od, Sm::OD, step128, w, Sm::W, step64);
+    // (dS's tile takes S0's place; its product is issued below)
+  }
+  __syncwarp();
+  pass_wait(&sm.done[0], 0, &sm.dead, p.status);
+  const int j = 32 * (warp & 3) + lane, half = warp >> 2;      // this thread's lane, and its half of the columns
+  const uint32_t lanes = tm + ((uint32_t)(32 * (warp & 3)) << 16);
+  const float inv_s0 = sm.inv_s[j < DK ? j : 0];
+  __syncthreads();
+  state_tile(dS, true);
+  fence_proxy_async_smem();
+  __syncthreads();
+  if (tid == 0) {
+    const uint64_t w = umma_desc(smem_addr(sm.tile.w), 16), sx = umma_desc(smem_addr(sm.tile.sx), 16);
+    product_ss<DV / 16, umma_idesc(128, 64, false)>(tm + kSW, sx, Sm::SX, step128, w, Sm::W, step64);
+    umma_commit(&sm.done[1]);
+  }
+  __syncwarp();
+  pass_wait(&sm.done[1], 0, &sm.dead, p.status);
+  tmem_fence_after();
+  // ---- results and q, k into the tiles' place (the scales stay where they are)
+  const float inv_ds = sm.inv_s[j < DK ? j : 0];
+  const float E = tid < DK ? sm.Epart[tid] : 0.f;
+  __syncthreads();
+#pragma unroll 1
+  for (int x = 32 * half; x < 32 * half + 32; x += 16) {
+    float a[16], b[16], c[16], y[16];
+    tmem_ld16(lanes + kSO + x, a);
+    if constexpr (!M2) tmem_ld16(lanes + kSO + 64 + x, b);
+    tmem_ld16(lanes + kSW + x, c);
+    tmem_ld16(lanes + kXY + x, y);
+    tmem_wait_ld();
+    if (j < DK) {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const int i = x + e;
+        sm.out.dq[i * PK + j] = a[e] * (inv_s0 * sm.inv_od[i]);
+        if constexpr (!M2) sm.out.h[i * PK + j] = b[e] * (inv_s0 * sm.inv_od[kChunk + i]);
+        sm.out.c[i * PK + j] = c[e] * (inv_ds * sm.inv_w[i]);
+      }
+    }
+    // lane i: X_i. for i < 64, Y_(i-64). behind
+    const int i = j & 63;
+    float* xy = j < kChunk ? sm.xy.X : sm.xy.Y;
+    const float si = sm.inv_od[j];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const float v = y[e] * (si * sm.inv_w[x + e]);
+      xy[(x + e) * PX + i] = x + e < i ? v : 0.f;
+      if (x + e == i && j < kChunk) sm.xd[i] = v;
+    }
+  }
+  tmem_fence_before();
+  {
+    constexpr int LPK = DK / 8, RPK = kNT / LPK, ITK = kChunk / RPK;
+    const int rk = tid / LPK, ck0 = 8 * (tid % LPK);
+    float a[ITK][8], b[ITK][8];
+    const long long at = ((ck.first + rk) * p.HK + hk) * DK + ck0, stp = (long long)RPK * p.HK * DK;
+    act_ld8_rows(static_cast<const T*>(p.q) + at, stp, (n - rk + RPK - 1) / RPK, a);
+    act_ld8_rows(static_cast<const T*>(p.k) + at, stp, (n - rk + RPK - 1) / RPK, b);
+#pragma unroll
+    for (int it = 0; it < ITK; ++it) {
+      float* q = &sm.q[(rk + it * RPK) * PK + ck0];
+      float* k = &sm.k[(rk + it * RPK) * PK + ck0];
+      st4(q, make_float4(a[it][0], a[it][1], a[it][2], a[it][3]));
+      st4(q + 4, make_float4(a[it][4], a[it][5], a[it][6], a[it][7]));
+      st4(k, make_float4(b[it][0], b[it][1], b[it][2], b[it][3]));
+      st4(k + 4, make_float4(b[it][4], b[it][5], b[it][6], b[it][7]));
+    }
+  }
+  __syncthreads();
+  if (warp == 0) {
+    tmem_fence_after();
+    tmem_free(tm, 256);
+  }
+  grad_sums<FORM, DK>(p, ck, h, sm, E);
+}
+
 __global__ void __launch_bounds__(256) scan_share_kernel(const ScanParams p) {
   const long long per = p.tokens * p.HK * (p.dk / 4);
   const int rep = p.H / p.HK;
@@ -409,13 +622,38 @@ int launch_grad_t(const ScanParams& p, cudaStream_t st) {
   return cudaGetLastError() == cudaSuccess ? SEED_OK : SEED_ERR_CUDA;
 }
 
+template <int FORM, int DK, int DV, typename T>
+int launch_grad_umma_t(const ScanParams& p, cudaStream_t st) {
+  static LaunchCache cache;
+  constexpr size_t need = sizeof(GradUmmaSmem<DK, DV>) + 1024;
+  constexpr size_t bytes = need < 116 * 1024 ? 116 * 1024 : need;      // one block per SM: tensor memory
+  static_assert(bytes <= 227 * 1024, "shared memory");
+  int dev;
+  if (int rc = cache.prepare(reinterpret_cast<const void*>(scan_grad_umma_kernel<FORM, DK, DV, T>), bytes, &dev)) return rc;
+  scan_grad_umma_kernel<FORM, DK, DV, T><<<(unsigned)(p.slots * p.H), kNT, bytes, st>>>(p);
+  return cudaGetLastError() == cudaSuccess ? SEED_OK : SEED_ERR_CUDA;
+}
+
 }  // namespace
 
 int launch_scan_grad(const ScanParams& p, int form, cudaStream_t st) {
+  if (p.dk >= 64 && p.dv >= 64) {
+    return with_factor_type_of(p.elem, [&](auto t) -> int {
+      using T = decltype(t);
+#define SEED_GRAD(F, K, V) \
+  if (form == F && p.dk == K && p.dv == V) return launch_grad_umma_t<F, K, V, T>(p, st);
+#define SEED_GRAD_D(F) SEED_GRAD(F, 64, 64) SEED_GRAD(F, 128, 128) SEED_GRAD(F, 128, 64) SEED_GRAD(F, 64, 128)
+      SEED_GRAD_D(SEED_GDN)
+      SEED_GRAD_D(SEED_KDA)
+      SEED_GRAD_D(SEED_MAMBA2)
+#undef SEED_GRAD_D
+#undef SEED_GRAD
+      return SEED_ERR_SHAPE;
+    });
+  }
 #define SEED_GRAD(F, K, V) \
   if (form == F && p.dk == K && p.dv == V) return launch_grad_t<F, K, V>(p, st);
-#define SEED_GRAD_D(F) \
-  SEED_GRAD(F, 16, 16) SEED_GRAD(F, 32, 32) SEED_GRAD(F, 64, 64) SEED_GRAD(F, 128, 128) SEED_GRAD(F, 128, 64) SEED_GRAD(F, 64, 128)
+#define SEED_GRAD_D(F) SEED_GRAD(F, 16, 16) SEED_GRAD(F, 32, 32)
   SEED_GRAD_D(SEED_GDN)
   SEED_GRAD_D(SEED_KDA)
   SEED_GRAD_D(SEED_MAMBA2)

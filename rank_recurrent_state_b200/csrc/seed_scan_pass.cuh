@@ -116,6 +116,18 @@ SEED_DEV void product(uint32_t d, uint32_t a, uint32_t a_lo, uint64_t tile, uint
   }
 }
 
+// The same with both operands in shared memory, two terms each.
+template <int KS, uint32_t IDESC, typename StepA, typename StepB>
+SEED_DEV void product_ss(uint32_t d, uint64_t a, uint32_t a_lo, StepA step_a, uint64_t b, uint32_t b_lo, StepB step_b) {
+#pragma unroll
+  for (int t = 0; t < 3; ++t) {
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks)
+      umma_ss(d, a + (((t == 1 ? a_lo : 0u) + step_a(ks)) >> 4), b + (((t == 2 ? b_lo : 0u) + step_b(ks)) >> 4), IDESC,
+              t + ks > 0);
+  }
+}
+
 // T: activation type.  SAVE: the backward pass's recomputation, which writes w and the
 // state before each chunk instead of o and S_out.  (Both are template parameters for the
 // size of the loop's code: it is walked once per chunk, and from beyond the instruction
