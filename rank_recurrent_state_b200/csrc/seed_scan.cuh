@@ -186,12 +186,20 @@ struct ChunkAt {
   bool last;              // the sequence's last chunk
 };
 SEED_DEV bool chunk_at(const ScanParams& p, int slot, ChunkAt* c) {
-  int lo = 0, hi = p.seqs - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    const int off = p.offsets[mid];
-    if ((off < 0 ? 0 : off / kChunk) + mid <= slot) lo = mid;
-    else hi = mid - 1;
+  // whole warps: the last sequence whose first slot is not behind `slot`, 32 probes a step
+  const int lane = threadIdx.x & 31;
+  int lo = 0, n = p.seqs;
+  while (n > 1) {
+    const int step = (n + 31) / 32, at = lane * step;
+    bool in = at < n;
+    if (in) {
+      const int off = p.offsets[lo + at];
+      in = (off < 0 ? 0 : off / kChunk) + lo + at <= slot;
+    }
+    const unsigned below = __ballot_sync(0xffffffffu, in);
+    const int last = below ? 31 - __clz(below) : 0;
+    lo += last * step;
+    n = min(step, n - last * step);
   }
   const SeqRange r = seq_range(p, lo, false);
   const int i = slot - r.slot0;

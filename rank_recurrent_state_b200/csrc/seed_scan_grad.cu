@@ -53,7 +53,7 @@ SEED_DEV float lanes_sum(float x) { return group_sum<G>(x); }
 
 // The sums over the chunk, the outputs and the decays' gradients, from q, k, the state's
 // products (sm.out), X and Y (sm.xy) in shared memory.  E: (S0 dS^T)_cc in thread c < DK.
-template <int FORM, int DK, typename Sm>
+template <int FORM, int DK, int NT, typename Sm>
 SEED_DEV void grad_sums(const ScanParams& p, const ChunkAt& ck, int h, Sm& sm, float E) {
   constexpr bool KDA = FORM == SEED_KDA, M2 = FORM == SEED_MAMBA2;
   constexpr int PK = Sm::PK, PX = Sm::PX;
@@ -61,7 +61,7 @@ SEED_DEV void grad_sums(const ScanParams& p, const ChunkAt& ck, int h, Sm& sm, f
   const int n = ck.n, hk = h / (p.H / p.HK);
   const float* al = p.alpha;
   // ---- sums over the chunk: a thread owns channel c and every NG-th block of 4 rows
-  constexpr int NG = kNT / DK;
+  constexpr int NG = NT / DK;
   constexpr int LG = DK < 32 ? DK : 32;
   const int c = tid % DK, grp = tid / DK;
   const float* arow = KDA ? al + (ck.first * p.H + h) * DK + c : nullptr;
@@ -75,6 +75,7 @@ SEED_DEV void grad_sums(const ScanParams& p, const ChunkAt& ck, int h, Sm& sm, f
     // rows i0 .. i0+3 against columns j <= i0, then the few inside the block
     float sq[4] = {}, sh[4] = {};
     float f = 1.f;
+#pragma unroll 4
     for (int j = i0; j >= 0; --j) {
       const float t = f * sm.k[j * PK + c];
       const float4 x = ld4(&sm.xy.X[j * PX + i0]);
@@ -111,6 +112,7 @@ SEED_DEV void grad_sums(const ScanParams& p, const ChunkAt& ck, int h, Sm& sm, f
     // columns i0 .. i0+3 against rows m >= i0+3, then the few inside the block
     float sc[4] = {};
     f = 1.f;
+#pragma unroll 4
     for (int m = i0 + 3; m < kChunk; ++m) {
       const float tq = f * sm.q[m * PK + c];
       const float tk = M2 ? 0.f : -f * sm.beta[m] * sm.k[m * PK + c];
@@ -193,6 +195,7 @@ SEED_DEV void grad_sums(const ScanParams& p, const ChunkAt& ck, int h, Sm& sm, f
     float e = 0.f;
     if (tid < DK) {
       float BC = 1.f;
+#pragma unroll 16
       for (int i = 0; i < n; ++i) BC *= dec(i);
       e = BC * E;
 #pragma unroll
@@ -390,7 +393,7 @@ __global__ void __launch_bounds__(kNT, 1) scan_grad_kernel(const ScanParams p) {
     }
   __syncthreads();
 
-  grad_sums<FORM, DK>(p, ck, h, sm, E);
+  grad_sums<FORM, DK, kNT>(p, ck, h, sm, E);
 }
 
 // The same with the products of the states, X and Y on the tensor cores (two-term fp16,
@@ -398,6 +401,9 @@ __global__ void __launch_bounds__(kNT, 1) scan_grad_kernel(const ScanParams p) {
 // the value channels: OD = [do; dw], W = w, and S0, then dS in the same place:
 //     S0 OD^T (key channel x 128 tokens), OD W^T (X and Y), dS W^T (key channel x 64 tokens)
 // The results replace the tiles in shared memory; the sums over the chunk are as above.
+// threads of the tensor-core kernel: its loops over shared memory are bound by latency
+constexpr int kGradThreads = 512;
+
 template <int DK, int DV>
 struct GradUmmaSmem {
   static constexpr int PK = DK + 4, PX = kChunk + 4;
@@ -414,7 +420,7 @@ struct GradUmmaSmem {
     };
   };
   float alpha[kChunk], beta[kChunk], kh[kChunk], xd[kChunk], val[8];
-  float E[kNT];
+  float E[kGradThreads];
   float red[8][kChunk][2];
   float inv_od[128], inv_w[kChunk], inv_s[128], Epart[128];
   uint64_t done[2];
@@ -423,9 +429,10 @@ struct GradUmmaSmem {
 };
 
 template <int FORM, int DK, int DV, typename T>
-__global__ void __launch_bounds__(kNT, 1) scan_grad_umma_kernel(const ScanParams p) {
+__global__ void __launch_bounds__(kGradThreads, 1) scan_grad_umma_kernel(const ScanParams p) {
   constexpr bool KDA = FORM == SEED_KDA, M2 = FORM == SEED_MAMBA2;
   using Sm = GradUmmaSmem<DK, DV>;
+  constexpr int kNT = kGradThreads;
   constexpr int PK = Sm::PK, PX = Sm::PX;
   extern __shared__ unsigned char smem_raw[];
   Sm& sm = *reinterpret_cast<Sm*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
@@ -520,7 +527,7 @@ __global__ void __launch_bounds__(kNT, 1) scan_grad_umma_kernel(const ScanParams
   }
   __syncwarp();
   pass_wait(&sm.done[0], 0, &sm.dead, p.status);
-  const int j = 32 * (warp & 3) + lane, half = warp >> 2;      // this thread's lane, and its half of the columns
+  const int j = 32 * (warp & 3) + lane, part = warp >> 2;      // this thread's lane, and its quarter of the columns
   const uint32_t lanes = tm + ((uint32_t)(32 * (warp & 3)) << 16);
   const float inv_s0 = sm.inv_s[j < DK ? j : 0];
   __syncthreads();
@@ -539,8 +546,8 @@ __global__ void __launch_bounds__(kNT, 1) scan_grad_umma_kernel(const ScanParams
   const float inv_ds = sm.inv_s[j < DK ? j : 0];
   const float E = tid < DK ? sm.Epart[tid] : 0.f;
   __syncthreads();
-#pragma unroll 1
-  for (int x = 32 * half; x < 32 * half + 32; x += 16) {
+  {
+    const int x = 16 * part;
     float a[16], b[16], c[16], y[16];
     tmem_ld16(lanes + kSO + x, a);
     if constexpr (!M2) tmem_ld16(lanes + kSO + 64 + x, b);
@@ -590,7 +597,7 @@ __global__ void __launch_bounds__(kNT, 1) scan_grad_umma_kernel(const ScanParams
     tmem_fence_after();
     tmem_free(tm, 256);
   }
-  grad_sums<FORM, DK>(p, ck, h, sm, E);
+  grad_sums<FORM, DK, kNT>(p, ck, h, sm, E);
 }
 
 __global__ void __launch_bounds__(256) scan_share_kernel(const ScanParams p) {
@@ -630,7 +637,7 @@ int launch_grad_umma_t(const ScanParams& p, cudaStream_t st) {
   static_assert(bytes <= 227 * 1024, "shared memory");
   int dev;
   if (int rc = cache.prepare(reinterpret_cast<const void*>(scan_grad_umma_kernel<FORM, DK, DV, T>), bytes, &dev)) return rc;
-  scan_grad_umma_kernel<FORM, DK, DV, T><<<(unsigned)(p.slots * p.H), kNT, bytes, st>>>(p);
+  scan_grad_umma_kernel<FORM, DK, DV, T><<<(unsigned)(p.slots * p.H), kGradThreads, bytes, st>>>(p);
   return cudaGetLastError() == cudaSuccess ? SEED_OK : SEED_ERR_CUDA;
 }
 

@@ -26,7 +26,8 @@ namespace seed {
 
 namespace {
 
-constexpr int kPrepThreads = 256;
+// Threads per block: with decays per channel the shared memory has room for one block per SM.
+__host__ __device__ constexpr int prep_threads(bool kda) { return kda ? 512 : 256; }
 constexpr int PX = kChunk + 4;
 
 // Element type of k and q in shared memory: 16-bit activations stay as they are; with
@@ -168,7 +169,7 @@ SEED_DEV void tile_rows(unsigned char* tile, int lo, int rows, int row0, float* 
 }
 
 // The tile of a 64 x 64 matrix (two terms, 8192 bytes apart) and its rows' inverse scales.
-SEED_DEV void store_square(unsigned char* img, float* inv, const float* M, int tid) {
+SEED_DEV void store_square(unsigned char* img, float* inv, const float* M, int tid) {      // 256 threads
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
     const int i = (tid >> 3) + 32 * half, c = 8 * (tid & 7);
@@ -213,9 +214,11 @@ SEED_DEV void invert(Sm& sm, int tid) {
     }
   }
   __syncthreads();
+  const bool on = tid < 256;      // of larger blocks the first 256 threads
   {      // two 32 x 32 blocks, each from its 16 x 16 quarters
-    const int b = 32 * (tid >> 7), e = tid & 127, i = e >> 3, c = 2 * (e & 7);
+    const int b = 32 * ((tid >> 7) & 1), e = tid & 127, i = e >> 3, c = 2 * (e & 7);
     float m0 = 0.f, m1 = 0.f;
+    if (on) {
 #pragma unroll
     for (int k = 0; k < 16; k += 4) {
       const float4 a = ld4(&A[(b + 16 + i) * PX + b + k]);
@@ -228,8 +231,10 @@ SEED_DEV void invert(Sm& sm, int tid) {
       }
     }
     *reinterpret_cast<float2*>(&M[(b / 2 + i) * 36 + c]) = make_float2(m0, m1);
+    }
     __syncthreads();
     m0 = m1 = 0.f;
+    if (on) {
 #pragma unroll
     for (int k = 0; k < 16; k += 4) {
       const float4 a = ld4(&T[(b + 16 + i) * PX + b + 16 + k]);
@@ -242,11 +247,13 @@ SEED_DEV void invert(Sm& sm, int tid) {
       }
     }
     *reinterpret_cast<float2*>(&T[(b + 16 + i) * PX + b + c]) = make_float2(m0, m1);
+    }
   }
   __syncthreads();
   {      // the 64 x 64 block from its 32 x 32 quarters
-    const int i = tid >> 3, c = 4 * (tid & 7);
+    const int i = (tid >> 3) & 31, c = 4 * (tid & 7);
     float4 m = zero4();
+    if (on) {
 #pragma unroll
     for (int k = 0; k < 32; k += 4) {
       const float4 a = ld4(&A[(32 + i) * PX + k]);
@@ -256,8 +263,10 @@ SEED_DEV void invert(Sm& sm, int tid) {
       m = fma4(a.w, ld4(&T[(k + 3) * PX + c]), m);
     }
     st4(&M[i * 36 + c], m);
+    }
     __syncthreads();
     m = zero4();
+    if (on) {
 #pragma unroll
     for (int k = 0; k < 32; k += 4) {
       const float4 a = ld4(&T[(32 + i) * PX + 32 + k]);
@@ -267,15 +276,16 @@ SEED_DEV void invert(Sm& sm, int tid) {
       m = fma4(-a.w, ld4(&M[(k + 3) * 36 + c]), m);
     }
     st4(&T[(32 + i) * PX + c], m);
+    }
   }
   __syncthreads();
 }
 
 template <int FORM, int DK, typename T>
-__global__ void __launch_bounds__(kPrepThreads) scan_prep_kernel(const ScanParams p) {
+__global__ void __launch_bounds__(prep_threads(FORM == SEED_KDA)) scan_prep_kernel(const ScanParams p) {
   constexpr bool KDA = FORM == SEED_KDA, M2 = FORM == SEED_MAMBA2;
   constexpr bool TWO = scan_two_terms(FORM, std::is_same<T, float>::value);
-  constexpr int kNT = kPrepThreads;
+  constexpr int kNT = prep_threads(KDA);
   using Sm = PrepSmem<KDA, DK, T>;
   using S = typename Sm::S;
   constexpr int PK = Sm::PK;
@@ -346,44 +356,35 @@ __global__ void __launch_bounds__(kPrepThreads) scan_prep_kernel(const ScanParam
       st4(&sm.in.a[i * PK + c], i < n ? ld4(arow + i * astep + c) : make_float4(1.f, 1.f, 1.f, 1.f));
     }
     __syncthreads();
-    // diagonal 16 x 16 blocks: a thread takes columns j and 15 - j of a block over a
-    // quarter of the channels (four channels in turn per lane), the decay running with i
-    if (tid < 128) {
-      const int b = 16 * (tid >> 5), pr = (tid >> 2) & 7, part = tid & 3;
-#pragma unroll 1
-      for (int side = 0; side < 2; ++side) {
-        const int j = side ? 15 - pr : pr;
-        float f[DK / 4];
+    // diagonal 16 x 16 blocks: a thread takes column j of a block over a quarter of the
+    // channels (four channels in turn per lane), for q or for k, the decay running with i
+    {
+      const int b = 16 * ((tid >> 6) & 3), j = (tid >> 2) & 15, part = tid & 3;
+      const bool isq = tid >= 256;
+      const float* X = isq ? sm.in.q : sm.in.k;
+      float* G = isq ? sm.QK : sm.KK;
+      float f[DK / 4];
 #pragma unroll
-        for (int x = 0; x < DK / 16; ++x) {
-          const float4 v = ld4(&sm.in.k[(b + j) * PK + 16 * x + 4 * part]);
-          f[4 * x] = v.x; f[4 * x + 1] = v.y; f[4 * x + 2] = v.z; f[4 * x + 3] = v.w;
-        }
-        for (int i = side ? 8 : 0; i < 16; ++i) {
-          float sq = 0.f, sk = 0.f;
-          if (i >= j) {
+      for (int x = 0; x < DK / 16; ++x) {
+        const float4 v = ld4(&sm.in.k[(b + j) * PK + 16 * x + 4 * part]);
+        f[4 * x] = v.x; f[4 * x + 1] = v.y; f[4 * x + 2] = v.z; f[4 * x + 3] = v.w;
+      }
+      for (int i = j & 8; i < 16; ++i) {      // (the warp's columns are 0-7 or 8-15)
+        float sum = 0.f;
+        if (i >= j) {
 #pragma unroll
-            for (int x = 0; x < DK / 16; ++x) {
-              const int at = (b + i) * PK + 16 * x + 4 * part;
-              if (i > j) {
-                const float4 a = ld4(&sm.in.a[at]);
-                f[4 * x] *= a.x; f[4 * x + 1] *= a.y; f[4 * x + 2] *= a.z; f[4 * x + 3] *= a.w;
-              }
-              const float4 qq = ld4(&sm.in.q[at]), kk = ld4(&sm.in.k[at]);
-              const float4 ff = make_float4(f[4 * x], f[4 * x + 1], f[4 * x + 2], f[4 * x + 3]);
-              sq += dot4(qq, ff);
-              sk += dot4(kk, ff);
+          for (int x = 0; x < DK / 16; ++x) {
+            const int at = (b + i) * PK + 16 * x + 4 * part;
+            if (i > j) {
+              const float4 a = ld4(&sm.in.a[at]);
+              f[4 * x] *= a.x; f[4 * x + 1] *= a.y; f[4 * x + 2] *= a.z; f[4 * x + 3] *= a.w;
             }
-          }
-          sq += __shfl_xor_sync(0xffffffffu, sq, 1);
-          sq += __shfl_xor_sync(0xffffffffu, sq, 2);
-          sk += __shfl_xor_sync(0xffffffffu, sk, 1);
-          sk += __shfl_xor_sync(0xffffffffu, sk, 2);
-          if (i >= j && part == 0) {
-            sm.QK[(b + i) * PX + b + j] = sq;
-            sm.KK[(b + i) * PX + b + j] = sk;
+            sum += dot4(ld4(&X[at]), make_float4(f[4 * x], f[4 * x + 1], f[4 * x + 2], f[4 * x + 3]));
           }
         }
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        if (i >= j && part == 0) G[(b + i) * PX + b + j] = sum;
       }
     }
     __syncthreads();
@@ -422,10 +423,9 @@ __global__ void __launch_bounds__(kPrepThreads) scan_prep_kernel(const ScanParam
     __syncthreads();
     if (tid < DK) sm.mv[2][tid] = sm.mv[0][tid] * sm.mv[1][tid];
     __syncthreads();
-    // 24 tiles left of the diagonal blocks, three per warp
+    // 24 tiles left of the diagonal blocks
 #pragma unroll 1
-    for (int e = 0; e < 3; ++e) {
-      const int x = 3 * warp + e;
+    for (int x = warp; x < 24; x += kNT / 32) {
       const bool isq = x < 12;
       const int y = isq ? x : x - 12;
       const int I = y < 2 ? 1 : y < 6 ? 2 : 3;
@@ -509,7 +509,7 @@ __global__ void __launch_bounds__(kPrepThreads) scan_prep_kernel(const ScanParam
         if (tid == kChunk - 1) *reinterpret_cast<float*>(tri + kTriEnd) = f;
       }
     }
-    {      // a thread takes column j of a block of 16 rows, the decay running down
+    if (tid < 256) {      // a thread takes column j of a block of 16 rows, the decay running down
       const int j = tid & 63, ib = tid >> 6, jb = j >> 4;
       float f = 1.f;
       if constexpr (!KDA) {
@@ -528,11 +528,11 @@ __global__ void __launch_bounds__(kPrepThreads) scan_prep_kernel(const ScanParam
     }
     if constexpr (!M2) {
       invert(sm, tid);
-      store_square(tri, vec + kVecT * kChunk, sm.t.T, tid);
+      if (tid < 256) store_square(tri, vec + kVecT * kChunk, sm.t.T, tid);
     } else {
       __syncthreads();
     }
-    store_square(tri + 16384, vec + kVecP * kChunk, sm.t.P, tid);
+    if (tid >= kNT - 256) store_square(tri + 16384, vec + kVecP * kChunk, sm.t.P, tid - (kNT - 256));
     __syncthreads();
   }
 }
@@ -544,7 +544,7 @@ int launch_prep_t(const ScanParams& p, cudaStream_t st) {
   int dev;
   if (int rc = cache.prepare(reinterpret_cast<const void*>(scan_prep_kernel<FORM, DK, T>), bytes, &dev)) return rc;
   const int blocks = p.slots * (FORM == SEED_KDA ? p.H : p.HK);
-  scan_prep_kernel<FORM, DK, T><<<blocks, kPrepThreads, bytes, st>>>(p);
+  scan_prep_kernel<FORM, DK, T><<<blocks, prep_threads(FORM == SEED_KDA), bytes, st>>>(p);
   return cudaGetLastError() == cudaSuccess ? SEED_OK : SEED_ERR_CUDA;
 }
 
