@@ -118,6 +118,31 @@ SEED_DEV void gram_store(const float (&c)[4], float* G, int r0, int n0, int lane
   *reinterpret_cast<float2*>(&G[(r0 + g + 8) * PX + n0 + 2 * t]) = make_float2(c[2], c[3]);
 }
 
+// A 16 x 8 tile of X Y over K terms, X [16][K] and Y [K][8] in shared memory, both as two
+// tf32 terms; and its store, times f.
+template <int K>
+SEED_DEV void tile_product(float (&c)[4], const float* X, int px, const float* Y, int py, int lane) {
+  const int g = lane >> 2, t = lane & 3;
+  c[0] = c[1] = c[2] = c[3] = 0.f;
+#pragma unroll
+  for (int k = 0; k < K; k += 8) {
+    const float a[4] = {X[g * px + k + t], X[(g + 8) * px + k + t], X[g * px + k + t + 4], X[(g + 8) * px + k + t + 4]};
+    const float b[2] = {Y[(k + t) * py + g], Y[(k + t + 4) * py + g]};
+    const float ah[4] = {tf32_hi(a[0]), tf32_hi(a[1]), tf32_hi(a[2]), tf32_hi(a[3])};
+    const float al[4] = {a[0] - ah[0], a[1] - ah[1], a[2] - ah[2], a[3] - ah[3]};
+    const float bh[2] = {tf32_hi(b[0]), tf32_hi(b[1])};
+    const float bl[2] = {b[0] - bh[0], b[1] - bh[1]};
+    mma_tf32(c, al, bh);
+    mma_tf32(c, ah, bl);
+    mma_tf32(c, ah, bh);
+  }
+}
+SEED_DEV void tile_store(const float (&c)[4], float* D, int pd, float f, int lane) {
+  const int g = lane >> 2, t = lane & 3;
+  *reinterpret_cast<float2*>(&D[g * pd + 2 * t]) = make_float2(f * c[0], f * c[1]);
+  *reinterpret_cast<float2*>(&D[(g + 8) * pd + 2 * t]) = make_float2(f * c[2], f * c[3]);
+}
+
 // Eight values of row `row` of a tile whose panels of 64 channels hold `rows` rows, from
 // channel c0 on, already scaled; two: the second term `lo` bytes behind.
 template <bool TWO>
@@ -214,68 +239,35 @@ SEED_DEV void invert(Sm& sm, int tid) {
     }
   }
   __syncthreads();
-  const bool on = tid < 256;      // of larger blocks the first 256 threads
+  // The blocks left of the diagonal by warp-level matrix products, a 16 x 8 tile per warp:
+  // M = A21 T11, T21 = -T22 M.  (In float32 FMA from shared memory these two products took
+  // 2,500 of the 8,700 shared-memory wavefronts of a chunk and head.)
+  const int warp = tid >> 5, lane = tid & 31;
   {      // two 32 x 32 blocks, each from its 16 x 16 quarters
-    const int b = 32 * ((tid >> 7) & 1), e = tid & 127, i = e >> 3, c = 2 * (e & 7);
-    float m0 = 0.f, m1 = 0.f;
-    if (on) {
-#pragma unroll
-    for (int k = 0; k < 16; k += 4) {
-      const float4 a = ld4(&A[(b + 16 + i) * PX + b + k]);
-      const float av[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-      for (int y = 0; y < 4; ++y) {
-        const float2 t = *reinterpret_cast<const float2*>(&T[(b + k + y) * PX + b + c]);
-        m0 = fmaf(av[y], t.x, m0);
-        m1 = fmaf(av[y], t.y, m1);
-      }
-    }
-    *reinterpret_cast<float2*>(&M[(b / 2 + i) * 36 + c]) = make_float2(m0, m1);
+    const int b = 32 * ((warp >> 1) & 1), n0 = 8 * (warp & 1);
+    float c[4];
+    if (warp < 4) {
+      tile_product<16>(c, &A[(b + 16) * PX + b], PX, &T[b * PX + b + n0], PX, lane);
+      tile_store(c, &M[(b / 2) * 36 + n0], 36, 1.f, lane);
     }
     __syncthreads();
-    m0 = m1 = 0.f;
-    if (on) {
-#pragma unroll
-    for (int k = 0; k < 16; k += 4) {
-      const float4 a = ld4(&T[(b + 16 + i) * PX + b + 16 + k]);
-      const float av[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-      for (int y = 0; y < 4; ++y) {
-        const float2 t = *reinterpret_cast<const float2*>(&M[(b / 2 + k + y) * 36 + c]);
-        m0 = fmaf(-av[y], t.x, m0);
-        m1 = fmaf(-av[y], t.y, m1);
-      }
-    }
-    *reinterpret_cast<float2*>(&T[(b + 16 + i) * PX + b + c]) = make_float2(m0, m1);
+    if (warp < 4) {
+      tile_product<16>(c, &T[(b + 16) * PX + b + 16], PX, &M[(b / 2) * 36 + n0], 36, lane);
+      tile_store(c, &T[(b + 16) * PX + b + n0], PX, -1.f, lane);
     }
   }
   __syncthreads();
   {      // the 64 x 64 block from its 32 x 32 quarters
-    const int i = (tid >> 3) & 31, c = 4 * (tid & 7);
-    float4 m = zero4();
-    if (on) {
-#pragma unroll
-    for (int k = 0; k < 32; k += 4) {
-      const float4 a = ld4(&A[(32 + i) * PX + k]);
-      m = fma4(a.x, ld4(&T[k * PX + c]), m);
-      m = fma4(a.y, ld4(&T[(k + 1) * PX + c]), m);
-      m = fma4(a.z, ld4(&T[(k + 2) * PX + c]), m);
-      m = fma4(a.w, ld4(&T[(k + 3) * PX + c]), m);
-    }
-    st4(&M[i * 36 + c], m);
+    const int i0 = 16 * ((warp >> 2) & 1), n0 = 8 * (warp & 3);
+    float c[4];
+    if (warp < 8) {
+      tile_product<32>(c, &A[(32 + i0) * PX], PX, &T[n0], PX, lane);
+      tile_store(c, &M[i0 * 36 + n0], 36, 1.f, lane);
     }
     __syncthreads();
-    m = zero4();
-    if (on) {
-#pragma unroll
-    for (int k = 0; k < 32; k += 4) {
-      const float4 a = ld4(&T[(32 + i) * PX + 32 + k]);
-      m = fma4(-a.x, ld4(&M[k * 36 + c]), m);
-      m = fma4(-a.y, ld4(&M[(k + 1) * 36 + c]), m);
-      m = fma4(-a.z, ld4(&M[(k + 2) * 36 + c]), m);
-      m = fma4(-a.w, ld4(&M[(k + 3) * 36 + c]), m);
-    }
-    st4(&T[(32 + i) * PX + c], m);
+    if (warp < 8) {
+      tile_product<32>(c, &T[(32 + i0) * PX + 32], PX, &M[n0], 36, lane);
+      tile_store(c, &T[(32 + i0) * PX + n0], PX, -1.f, lane);
     }
   }
   __syncthreads();
