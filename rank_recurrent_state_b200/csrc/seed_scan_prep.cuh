@@ -184,7 +184,12 @@ SEED_DEV void tile_rows(unsigned char* tile, int lo, int rows, int row0, float* 
     const int i = r0 + it * RPI;
     float y[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] = f == nullptr ? x[it][e] : x[it][e] * f[i * pitch + c0 + e];
+    for (int e = 0; e < 8; ++e) y[e] = x[it][e];
+    if (f != nullptr) {
+      const float4 a = ld4(f + i * pitch + c0), b = ld4(f + i * pitch + c0 + 4);
+      y[0] *= a.x; y[1] *= a.y; y[2] *= a.z; y[3] *= a.w;
+      y[4] *= b.x; y[5] *= b.y; y[6] *= b.z; y[7] *= b.w;
+    }
     const float s = pow2_scale(row_max<LPR>(y));
     if (c0 == 0) inv[i] = pow2_inverse(s);
 #pragma unroll
@@ -348,35 +353,44 @@ __global__ void __launch_bounds__(prep_threads(FORM == SEED_KDA)) scan_prep_kern
       st4(&sm.in.a[i * PK + c], i < n ? ld4(arow + i * astep + c) : make_float4(1.f, 1.f, 1.f, 1.f));
     }
     __syncthreads();
-    // diagonal 16 x 16 blocks: a thread takes column j of a block over a quarter of the
-    // channels (four channels in turn per lane), for q or for k, the decay running with i
-    {
-      const int b = 16 * ((tid >> 6) & 3), j = (tid >> 2) & 15, part = tid & 3;
-      const bool isq = tid >= 256;
-      const float* X = isq ? sm.in.q : sm.in.k;
-      float* G = isq ? sm.QK : sm.KK;
-      float f[DK / 4];
+    // diagonal 16 x 16 blocks, two warps each: a thread takes two columns over an eighth of
+    // the channels (four channels in turn per lane), the decays running with row i
+    if (warp < 8) {
+      const int b = 16 * (warp >> 1), part = lane & 7, g = lane >> 3;
+      const int col[2] = {(warp & 1) ? 7 - g : g, (warp & 1) ? 8 + g : 15 - g};
+      float f[2][DK / 8] = {};
+      float* out = (part & 4) ? sm.KK : sm.QK;
+      const int out_col = b + ((part & 2) ? col[1] : col[0]);
+#pragma unroll 2
+      for (int i = 0; i < 16; ++i) {
+        float v[4] = {};      // q with column 0, column 1, k with column 0, column 1
 #pragma unroll
-      for (int x = 0; x < DK / 16; ++x) {
-        const float4 v = ld4(&sm.in.k[(b + j) * PK + 16 * x + 4 * part]);
-        f[4 * x] = v.x; f[4 * x + 1] = v.y; f[4 * x + 2] = v.z; f[4 * x + 3] = v.w;
-      }
-      for (int i = j & 8; i < 16; ++i) {      // (the warp's columns are 0-7 or 8-15)
-        float sum = 0.f;
-        if (i >= j) {
+        for (int x = 0; x < DK / 32; ++x) {
+          const int at = (b + i) * PK + 32 * x + 4 * part;
+          const float4 a = ld4(&sm.in.a[at]), qq = ld4(&sm.in.q[at]), kk = ld4(&sm.in.k[at]);
+          const float av[4] = {a.x, a.y, a.z, a.w}, qv[4] = {qq.x, qq.y, qq.z, qq.w}, kv[4] = {kk.x, kk.y, kk.z, kk.w};
 #pragma unroll
-          for (int x = 0; x < DK / 16; ++x) {
-            const int at = (b + i) * PK + 16 * x + 4 * part;
-            if (i > j) {
-              const float4 a = ld4(&sm.in.a[at]);
-              f[4 * x] *= a.x; f[4 * x + 1] *= a.y; f[4 * x + 2] *= a.z; f[4 * x + 3] *= a.w;
+          for (int y = 0; y < 2; ++y) {
+            const bool starts = i == col[y];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              float& ff = f[y][4 * x + e];
+              ff = starts ? kv[e] : ff * av[e];      // zero above the diagonal
+              v[y] = fmaf(qv[e], ff, v[y]);
+              v[2 + y] = fmaf(kv[e], ff, v[2 + y]);
             }
-            sum += dot4(ld4(&X[at]), make_float4(f[4 * x], f[4 * x + 1], f[4 * x + 2], f[4 * x + 3]));
           }
         }
-        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-        if (i >= j && part == 0) G[(b + i) * PX + b + j] = sum;
+        // four sums over eight lanes by halving: lane bits 4 and 2 pick the value
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          const float send = (part & 4) ? v[y] : v[2 + y], keep = (part & 4) ? v[2 + y] : v[y];
+          v[y] = keep + __shfl_xor_sync(0xffffffffu, send, 4);
+        }
+        const float send = (part & 2) ? v[0] : v[1], keep = (part & 2) ? v[1] : v[0];
+        float t = keep + __shfl_xor_sync(0xffffffffu, send, 2);
+        t += __shfl_xor_sync(0xffffffffu, t, 1);
+        if (!(part & 1)) out[(b + i) * PX + out_col] = t;
       }
     }
     __syncthreads();
@@ -457,40 +471,46 @@ __global__ void __launch_bounds__(prep_threads(FORM == SEED_KDA)) scan_prep_kern
   }
   __syncthreads();
 
+  float be_next = 0.f, al_next = 1.f;      // token tid's, of the next head
+  auto fetch = [&](int h) {
+    if (tid < n) {
+      be_next = p.beta[(ck.first + tid) * p.H + h];
+      if constexpr (!KDA) al_next = p.alpha[(ck.first + tid) * p.H + h];
+    }
+  };
+  fetch(KDA ? grp : hk * rep);
   for (int r = 0; r < (KDA ? 1 : rep); ++r) {
     const int h = KDA ? grp : hk * rep + r;
     unsigned char* tri = p.tri + ((long long)slot * p.H + h) * kTriBytes;
     float* vec = reinterpret_cast<float*>(tri + kTriVec);
     if (tid < kChunk) {
-      const bool in = tid < n;
-      const float be = in ? p.beta[(ck.first + tid) * p.H + h] : 0.f;
-      sm.beta[tid] = be;
-      vec[kVecBeta * kChunk + tid] = be;
+      sm.beta[tid] = be_next;
+      vec[kVecBeta * kChunk + tid] = be_next;
       if constexpr (KDA) {
         vec[kVecK * kChunk + tid] = sm.invK[tid];
         vec[kVecQ * kChunk + tid] = sm.invQ[tid];
         vec[kVecE * kChunk + tid] = sm.invE[tid];
       } else {
-        sm.alpha[tid] = in ? p.alpha[(ck.first + tid) * p.H + h] : 1.f;
+        // products within blocks of 16 tokens: up to the token, and behind it
+        sm.alpha[tid] = al_next;
+        float f = al_next, g = al_next;
+#pragma unroll
+        for (int off = 1; off < 16; off <<= 1) {
+          const float x = __shfl_up_sync(0xffffffffu, f, off, 16), y = __shfl_down_sync(0xffffffffu, g, off, 16);
+          if ((tid & 15) >= off) f *= x;
+          if ((tid & 15) + off < 16) g *= y;
+        }
+        g = __shfl_down_sync(0xffffffffu, g, 1, 16);
+        sm.B[tid] = f;
+        sm.G[tid] = (tid & 15) == 15 ? 1.f : g;
+        if ((tid & 15) == 15) sm.blk[tid >> 4] = f;
       }
     }
     for (int e = tid; e < kChunk * kChunk / 4; e += kNT) st4(&sm.t.T[(e / 16) * PX + 4 * (e % 16)], zero4());
+    if (!KDA && r + 1 < rep) fetch(h + 1);
     __syncthreads();
     if constexpr (!KDA) {
-      // products within blocks of 16 tokens, then over the blocks
-      if (tid < kChunk) {
-        const int b = tid & ~15;
-        float f = 1.f, g = 1.f;
-        for (int s = b; s < b + 16; ++s) {
-          if (s <= tid) f *= sm.alpha[s];
-          if (s > tid) g *= sm.alpha[s];
-        }
-        sm.B[tid] = f;
-        sm.G[tid] = g;
-        if (tid == b + 15) sm.blk[tid >> 4] = f;
-      }
-      __syncthreads();
-      if (tid < kChunk) {
+      if (tid < kChunk) {      // over the blocks
         const int b = tid >> 4;
         float f = sm.B[tid], g = sm.G[tid];
         for (int x = 0; x < b; ++x) f *= sm.blk[x];
