@@ -16,7 +16,7 @@
 // value), which leaves k_t . D_tj k_j, q_t . D_tj k_j and the decayed k_t, q_t; the dot
 // products with the stored columns are a small product from shared memory; then each
 // thread owns a value channel and resolves the nodes in order.
-#include "seed_common.cuh"
+#include "seed_decode.cuh"
 
 namespace seed {
 
@@ -52,23 +52,26 @@ struct TreeSmem {
     us = xs + rows * (dk + 4);
     const int u1 = ((m + 1 + 3) & ~3) * (dk + 4), w1 = N * dv;
     ys = us + (u1 > w1 ? u1 : w1);
-    kk = ys + (m + 1) * rows;
+    const int y1 = (m + 1) * rows, k1 = N * (dk + 4);
+    kk = ys + (y1 > k1 ? y1 : k1);
     pp = kk + N * N;
     total = pp + N * N;
   }
 };
 
-template <int FORM, typename TS>
+template <int FORM, int DK, int DV, typename TS>
 __global__ void __launch_bounds__(kNT) decode_tree_kernel(const TreeParams p) {
   constexpr bool KDA = FORM == SEED_KDA, M2 = FORM == SEED_MAMBA2;
   extern __shared__ __align__(16) float smf[];
   __shared__ int s_par[SEED_MAX_NODES];
+  __shared__ float s_al[SEED_MAX_NODES], s_be[SEED_MAX_NODES];
   __shared__ unsigned long long s_anc[SEED_MAX_NODES];     // ancestors, the node itself left out
-  const int N = p.N, dk = p.dk, dv = p.dv, PK = dk + 4;
+  constexpr int dk = DK, dv = DV, PK = DK + 4, E = DK < 32 ? 1 : DK / 32;
+  const int N = p.N;
   const TreeSmem lay(N, p.m, dk, dv);
   float* xs = smf + lay.xs;      // rows t: decayed k_t; rows rows/2 + t: decayed q_t
   float* us = smf + lay.us;      // true U columns, then a; later w
-  float* ys = smf + lay.ys;      // [column][row]
+  float* ys = smf + lay.ys;      // the nodes' k; later [column][row]
   float* kk = smf + lay.kk;
   float* pp = smf + lay.pp;
   const int half = lay.rows / 2;
@@ -113,53 +116,74 @@ __global__ void __launch_bounds__(kNT) decode_tree_kernel(const TreeParams p) {
   // ---- stored columns (true U) and a, beside them
   const TS* U = static_cast<const TS*>(p.U) + unit * (long long)p.m * dk;
   const float* sc = p.scale + unit * p.slen;
-  for (int e = tid; e < c * (dk / 4); e += kNT) {
-    const int j = e / (dk / 4), i = 4 * (e % (dk / 4));
+  const long long row = (long long)b * N * p.H + h;     // token t: row + t H
+  constexpr int q4 = dk / 4;
+#pragma unroll 4
+  for (int e = tid; e < N * q4; e += kNT) {
+    const int t = e / q4, i = 4 * (e % q4);
+    st4(ys + t * PK + i, ld4(p.k + (row + (long long)t * p.H) * dk + i));
+  }
+#pragma unroll 4
+  for (int e = tid; e < c * q4; e += kNT) {
+    const int j = e / q4, i = 4 * (e % q4);
     float4 x = fac_ld4(U + (long long)j * dk + i);
     if constexpr (KDA) x = mul4(x, ld4(sc + i));
     else x = fma4(sc[j], x, zero4());
     st4(us + j * PK + i, x);
   }
   for (int i = tid; i < dk; i += kNT) us[c * PK + i] = p.a[unit * dk + i];
+  if (!KDA && tid < N) s_al[tid] = p.alpha[row + (long long)tid * p.H];
+  if (tid < N) s_be[tid] = p.beta[row + (long long)tid * p.H];
+  __syncthreads();
 
   // ---- paths
-  const long long row = (long long)b * N * p.H + h;     // token t: row + t H
   for (int t = warp; t < half; t += kNT / 32) {
-    float kt[4], qt[4], f[4];
+    float kt[E], qt[E], f[E];
     const bool used = t < N && s_par[t] >= -1;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
+    for (int e = 0; e < E; ++e) {
       const int i = lane + 32 * e;
-      kt[e] = used && i < dk ? p.k[(row + (long long)t * p.H) * dk + i] : 0.f;
+      kt[e] = used && i < dk ? ys[t * PK + i] : 0.f;
       qt[e] = used && i < dk ? p.q[(row + (long long)t * p.H) * dk + i] : 0.f;
       f[e] = 1.f;
     }
+    // four nodes of the path at a time: their eight dot products are summed over the warp
+    // together
     unsigned long long anc = 0;
-    for (int j = used ? t : -1; j >= 0; j = s_par[j]) {
-      if (j != t) anc |= 1ull << j;
-      const long long rj = row + (long long)j * p.H;
-      float sk = 0.f, sq = 0.f;
-      const float g = KDA ? 1.f : p.alpha[rj];
+    int j = used ? t : -1;
+    while (j >= 0) {
+      float v[8] = {};
+      int at[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int i = lane + 32 * e;
-        if (i < dk) {
-          const float kj = f[e] * p.k[rj * dk + i];
-          if constexpr (!M2) sk = fmaf(kt[e], kj, sk);
-          sq = fmaf(qt[e], kj, sq);
-          f[e] *= KDA ? p.alpha[rj * dk + i] : g;
+      for (int x = 0; x < 4; ++x) {
+        at[x] = j;
+        if (j >= 0) {
+          if (j != t) anc |= 1ull << j;
+          const float g = KDA ? 1.f : s_al[j];
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            const int i = lane + 32 * e;
+            if (i < dk) {
+              const float kj = f[e] * ys[j * PK + i];
+              if constexpr (!M2) v[4 + x] = fmaf(kt[e], kj, v[4 + x]);
+              v[x] = fmaf(qt[e], kj, v[x]);
+              f[e] *= KDA ? p.alpha[(row + (long long)j * p.H) * dk + i] : g;
+            }
+          }
+          j = s_par[j];
         }
       }
-      sq = group_sum<32>(sq);
-      if constexpr (!M2) sk = group_sum<32>(sk);
-      if (lane == 0) {
-        pp[t * N + j] = sq;
-        if (!M2 && j != t) kk[t * N + j] = sk;
+      const float tot = warp_xreduce<8>(v);      // value lane / 4
+      const int which = lane >> 2, node = at[0] * ((which & 3) == 0) + at[1] * ((which & 3) == 1) +
+                                          at[2] * ((which & 3) == 2) + at[3] * ((which & 3) == 3);
+      if ((lane & 3) == 0 && node >= 0) {
+        if (which < 4) pp[t * N + node] = tot;
+        else if (!M2) kk[t * N + node] = tot;
       }
     }
     if (lane == 0 && t < N) s_anc[t] = anc;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
+    for (int e = 0; e < E; ++e) {
       const int i = lane + 32 * e;
       if (i < dk) {
         xs[t * PK + i] = f[e] * kt[e];
@@ -169,25 +193,41 @@ __global__ void __launch_bounds__(kNT) decode_tree_kernel(const TreeParams p) {
   }
   __syncthreads();
 
-  // ---- ys[j][row] = x_row . (column j); column c is a.  Tiles of 4 rows x 2 columns.
-  const int ct = (c + 2) / 2;
-  for (int e = tid; e < (lay.rows / 4) * ct; e += kNT) {
-    const int r0 = 4 * (e % (lay.rows / 4)), j0 = 2 * (e / (lay.rows / 4));
-    const int j1 = j0 + 1 <= c ? j0 + 1 : j0;
-    float acc[4][2] = {};
-    if (!M2 || r0 + 3 >= half) {          // Mamba-2 reads the state with q alone
-      for (int i = 0; i < dk; i += 4) {
-        const float4 u0 = ld4(us + j0 * PK + i), u1 = ld4(us + j1 * PK + i);
+  // ---- ys[j][row] = x_row . (column j); column c is a.  Tiles of 4 rows x 4 columns, two
+  // lanes along the channels each.
+  const int ct = (c + 4) / 4;
+  for (int e0 = 0; e0 < (lay.rows / 4) * ct; e0 += kNT / 2) {
+    const int e = e0 + tid / 2, part = tid & 1;
+    const bool on = e < (lay.rows / 4) * ct;
+    const int r0 = on ? 4 * (e % (lay.rows / 4)) : 0, j0 = on ? 4 * (e / (lay.rows / 4)) : 0;
+    float acc[4][4] = {};
+    if (on && (!M2 || r0 + 3 >= half)) {          // Mamba-2 reads the state with q alone
+      const float* xr = xs + r0 * PK + 4 * part;
+      const float* ur = us + 4 * part;
+      int at[4];
+#pragma unroll
+      for (int y = 0; y < 4; ++y) at[y] = (j0 + y <= c ? j0 + y : c) * PK;
+#pragma unroll 4
+      for (int i = 0; i < dk; i += 8) {
+        float4 u[4];
+#pragma unroll
+        for (int y = 0; y < 4; ++y) u[y] = ld4(ur + at[y] + i);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const float4 x = ld4(xs + (r0 + r) * PK + i);
-          acc[r][0] += dot4(x, u0);
-          acc[r][1] += dot4(x, u1);
+          const float4 x = ld4(xr + r * PK + i);
+#pragma unroll
+          for (int y = 0; y < 4; ++y) acc[r][y] += dot4(x, u[y]);
         }
       }
     }
-    st4(ys + j0 * lay.rows + r0, make_float4(acc[0][0], acc[1][0], acc[2][0], acc[3][0]));
-    if (j1 != j0) st4(ys + j1 * lay.rows + r0, make_float4(acc[0][1], acc[1][1], acc[2][1], acc[3][1]));
+#pragma unroll
+    for (int y = 0; y < 4; ++y) {
+      const float4 o = make_float4(acc[0][y] + __shfl_xor_sync(0xffffffffu, acc[0][y], 1),
+                                   acc[1][y] + __shfl_xor_sync(0xffffffffu, acc[1][y], 1),
+                                   acc[2][y] + __shfl_xor_sync(0xffffffffu, acc[2][y], 1),
+                                   acc[3][y] + __shfl_xor_sync(0xffffffffu, acc[3][y], 1));
+      if (on && part == (y & 1) && j0 + y <= c) st4(ys + (j0 + y) * lay.rows + r0, o);
+    }
   }
   __syncthreads();
 
@@ -198,14 +238,23 @@ __global__ void __launch_bounds__(kNT) decode_tree_kernel(const TreeParams p) {
     const TS* V = static_cast<const TS*>(p.V) + unit * (long long)p.m * dv + col;
     const float vbc = vb[col];
     for (int t0 = 0; t0 < N; t0 += 8) {
-      float rk[8], rq[8];
+      float rk[8], rq[8], vt[8];
+#pragma unroll
+      for (int r = 0; r < 8; ++r) vt[r] = t0 + r < N ? p.v[(row + (long long)(t0 + r) * p.H) * dv + col] : 0.f;
 #pragma unroll
       for (int r = 0; r < 8; ++r) {
         rk[r] = vbc * ys[c * lay.rows + t0 + r];
         rq[r] = vbc * ys[c * lay.rows + half + t0 + r];
       }
-      for (int j = 0; j < c; ++j) {
-        const float vj = fac_to_f(V[(long long)j * dv]);
+      for (int j0 = 0; j0 < c; j0 += 8) {
+       float vc[8];
+#pragma unroll
+       for (int x = 0; x < 8; ++x) vc[x] = fac_to_f(V[(long long)(j0 + x < c ? j0 + x : c - 1) * dv]);
+#pragma unroll
+       for (int x = 0; x < 8; ++x) {
+        if (j0 + x >= c) break;
+        const int j = j0 + x;
+        const float vj = vc[x];
         const float* y = ys + j * lay.rows + t0;
         if constexpr (!M2) {
           const float4 a0 = ld4(y), a1 = ld4(y + 4);
@@ -219,6 +268,7 @@ __global__ void __launch_bounds__(kNT) decode_tree_kernel(const TreeParams p) {
         rq[2] = fmaf(b0.z, vj, rq[2]); rq[3] = fmaf(b0.w, vj, rq[3]);
         rq[4] = fmaf(b1.x, vj, rq[4]); rq[5] = fmaf(b1.y, vj, rq[5]);
         rq[6] = fmaf(b1.z, vj, rq[6]); rq[7] = fmaf(b1.w, vj, rq[7]);
+       }
       }
 #pragma unroll
       for (int r = 0; r < 8; ++r) {
@@ -228,7 +278,7 @@ __global__ void __launch_bounds__(kNT) decode_tree_kernel(const TreeParams p) {
           const bool used = s_par[t] >= -1;
           float w = 0.f, o = 0.f;
           if (used) {
-            float x = p.v[rt * dv + col];
+            float x = vt[r];
             o = rq[r];
             if constexpr (!M2) x -= rk[r];
             // ancestors alone: another branch's values (NaN, say) never come in
@@ -238,7 +288,7 @@ __global__ void __launch_bounds__(kNT) decode_tree_kernel(const TreeParams p) {
               if constexpr (!M2) x = fmaf(-kk[t * N + j], wj, x);
               o = fmaf(pp[t * N + j], wj, o);
             }
-            w = p.beta[rt] * x;
+            w = s_be[t] * x;
             o = fmaf(pp[t * N + t], w, o);
             bad = bad || !(isfinite(w) && isfinite(o));
           }
@@ -388,15 +438,15 @@ __global__ void __launch_bounds__(kNT) tree_commit_kernel(const CommitParams p) 
   if (bad) raise_flag(p.status, SEED_FLAG_NONFINITE);
 }
 
-template <int FORM, typename TS>
+template <int FORM, int DK, int DV, typename TS>
 int launch_tree_t(const TreeParams& p, cudaStream_t st) {
   static LaunchCache cache;
   const size_t bytes = sizeof(float) * (size_t)TreeSmem(p.N, p.m, p.dk, p.dv).total;
   constexpr size_t most = 220 * 1024;      // 64 nodes, 96 columns, d 128: 199 KB
   if (bytes > most) return SEED_ERR_SHAPE;
   int dev;
-  if (int rc = cache.prepare(reinterpret_cast<const void*>(decode_tree_kernel<FORM, TS>), most, &dev)) return rc;
-  decode_tree_kernel<FORM, TS><<<p.B * p.H, kNT, bytes, st>>>(p);
+  if (int rc = cache.prepare(reinterpret_cast<const void*>(decode_tree_kernel<FORM, DK, DV, TS>), most, &dev)) return rc;
+  decode_tree_kernel<FORM, DK, DV, TS><<<p.B * p.H, kNT, bytes, st>>>(p);
   return cudaGetLastError() == cudaSuccess ? SEED_OK : SEED_ERR_CUDA;
 }
 
@@ -415,12 +465,16 @@ int launch_decode_tree(const seed_dims& d, const seed_state& s, int layer, int n
                      d.batch, d.layers, d.heads, layer, d.R + d.W, scale_len(d), n_nodes, d.d_k, d.d_v};
   return with_factor_type(d, [&](auto t) -> int {
     using TS = decltype(t);
-    switch (d.form) {
-      case SEED_GDN: return launch_tree_t<SEED_GDN, TS>(p, st);
-      case SEED_KDA: return launch_tree_t<SEED_KDA, TS>(p, st);
-      case SEED_MAMBA2: return launch_tree_t<SEED_MAMBA2, TS>(p, st);
-    }
-    return SEED_ERR_INVALID_ARG;
+#define SEED_TREE(F, K, V) \
+  if (d.form == F && d.d_k == K && d.d_v == V) return launch_tree_t<F, K, V, TS>(p, st);
+#define SEED_TREE_D(F) \
+  SEED_TREE(F, 16, 16) SEED_TREE(F, 32, 32) SEED_TREE(F, 64, 64) SEED_TREE(F, 128, 128) SEED_TREE(F, 128, 64) SEED_TREE(F, 64, 128)
+    SEED_TREE_D(SEED_GDN)
+    SEED_TREE_D(SEED_KDA)
+    SEED_TREE_D(SEED_MAMBA2)
+#undef SEED_TREE_D
+#undef SEED_TREE
+    return SEED_ERR_SHAPE;
   });
 }
 
