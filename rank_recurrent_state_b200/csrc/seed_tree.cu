@@ -11,11 +11,13 @@
 // (Mamba-2: w_t = beta_t v_t).  So the stored columns are read once for all nodes,
 // and no node's d_k x d_v state is ever formed.
 //
-// One block per (request, head).  A warp walks a node's path to the root with the
-// running decay in registers (products, never quotients: a zero decay is an ordinary
-// value), which leaves k_t . D_tj k_j, q_t . D_tj k_j and the decayed k_t, q_t; the dot
-// products with the stored columns are a small product from shared memory; then each
-// thread owns a value channel and resolves the nodes in order.
+// One block per (request, head).  Decays are products along a node's path to the root,
+// never quotients (a zero decay is an ordinary value).  With one decay per head a thread
+// walks the path of each node, and the dot products of all nodes' k and q with the stored
+// columns, a and the nodes' k are one small product from shared memory.  With decays per
+// channel a warp walks the path with the running decays in registers, which leaves
+// k_t . D_tj k_j, q_t . D_tj k_j and the decayed k_t, q_t for the product with the columns.
+// Then each thread owns a value channel and resolves the nodes in order.
 #include "seed_decode.cuh"
 
 namespace seed {
@@ -64,14 +66,14 @@ __global__ void __launch_bounds__(kNT) decode_tree_kernel(const TreeParams p) {
   constexpr bool KDA = FORM == SEED_KDA, M2 = FORM == SEED_MAMBA2;
   extern __shared__ __align__(16) float smf[];
   __shared__ int s_par[SEED_MAX_NODES];
-  __shared__ float s_al[SEED_MAX_NODES], s_be[SEED_MAX_NODES];
+  __shared__ __align__(16) float s_al[SEED_MAX_NODES], s_be[SEED_MAX_NODES], s_B[SEED_MAX_NODES];
   __shared__ unsigned long long s_anc[SEED_MAX_NODES];     // ancestors, the node itself left out
   constexpr int dk = DK, dv = DV, PK = DK + 4, E = DK < 32 ? 1 : DK / 32;
   const int N = p.N;
   const TreeSmem lay(N, p.m, dk, dv);
-  float* xs = smf + lay.xs;      // rows t: decayed k_t; rows rows/2 + t: decayed q_t
+  float* xs = smf + lay.xs;      // rows t: k_t, rows rows/2 + t: q_t (KDA: decayed by B_t)
   float* us = smf + lay.us;      // true U columns, then a; later w
-  float* ys = smf + lay.ys;      // the nodes' k; later [column][row]
+  float* ys = smf + lay.ys;      // KDA: the nodes' k; then [column][row]
   float* kk = smf + lay.kk;
   float* pp = smf + lay.pp;
   const int half = lay.rows / 2;
@@ -118,10 +120,19 @@ __global__ void __launch_bounds__(kNT) decode_tree_kernel(const TreeParams p) {
   const float* sc = p.scale + unit * p.slen;
   const long long row = (long long)b * N * p.H + h;     // token t: row + t H
   constexpr int q4 = dk / 4;
+  if constexpr (KDA) {
 #pragma unroll 4
-  for (int e = tid; e < N * q4; e += kNT) {
-    const int t = e / q4, i = 4 * (e % q4);
-    st4(ys + t * PK + i, ld4(p.k + (row + (long long)t * p.H) * dk + i));
+    for (int e = tid; e < N * q4; e += kNT) {
+      const int t = e / q4, i = 4 * (e % q4);
+      st4(ys + t * PK + i, ld4(p.k + (row + (long long)t * p.H) * dk + i));
+    }
+  } else {
+#pragma unroll 4
+    for (int e = tid; e < lay.rows * q4; e += kNT) {
+      const int r = e / q4, i = 4 * (e % q4), t = r < half ? r : r - half;
+      const float* src = r < half ? p.k : p.q;
+      st4(xs + r * PK + i, t < N ? ld4(src + (row + (long long)t * p.H) * dk + i) : zero4());
+    }
   }
 #pragma unroll 4
   for (int e = tid; e < c * q4; e += kNT) {
@@ -137,7 +148,20 @@ __global__ void __launch_bounds__(kNT) decode_tree_kernel(const TreeParams p) {
   __syncthreads();
 
   // ---- paths
-  for (int t = warp; t < half; t += kNT / 32) {
+  if constexpr (!KDA) {
+    if (tid < half) {
+      float f = 1.f;
+      unsigned long long anc = 0;
+      for (int j = tid < N && s_par[tid] >= -1 ? tid : -1; j >= 0; j = s_par[j]) {
+        if (j != tid) anc |= 1ull << j;
+        kk[tid * N + j] = pp[tid * N + j] = f;      // D_tj, times the dot products below
+        f *= s_al[j];
+      }
+      s_B[tid] = f;
+      if (tid < N) s_anc[tid] = anc;
+    }
+  }
+  for (int t = KDA ? warp : half; t < half; t += kNT / 32) {
     float kt[E], qt[E], f[E];
     const bool used = t < N && s_par[t] >= -1;
 #pragma unroll
@@ -159,7 +183,6 @@ __global__ void __launch_bounds__(kNT) decode_tree_kernel(const TreeParams p) {
         at[x] = j;
         if (j >= 0) {
           if (j != t) anc |= 1ull << j;
-          const float g = KDA ? 1.f : s_al[j];
 #pragma unroll
           for (int e = 0; e < E; ++e) {
             const int i = lane + 32 * e;
@@ -167,7 +190,7 @@ __global__ void __launch_bounds__(kNT) decode_tree_kernel(const TreeParams p) {
               const float kj = f[e] * ys[j * PK + i];
               if constexpr (!M2) v[4 + x] = fmaf(kt[e], kj, v[4 + x]);
               v[x] = fmaf(qt[e], kj, v[x]);
-              f[e] *= KDA ? p.alpha[(row + (long long)j * p.H) * dk + i] : g;
+              f[e] *= p.alpha[(row + (long long)j * p.H) * dk + i];
             }
           }
           j = s_par[j];
@@ -193,9 +216,9 @@ __global__ void __launch_bounds__(kNT) decode_tree_kernel(const TreeParams p) {
   }
   __syncthreads();
 
-  // ---- ys[j][row] = x_row . (column j); column c is a.  Tiles of 4 rows x 4 columns, two
-  // lanes along the channels each.
-  const int ct = (c + 4) / 4;
+  // ---- ys[j][row] = x_row . (column j); column c is a, and with one decay per head the
+  // nodes' k follow.  Tiles of 4 rows x 4 columns, two lanes along the channels each.
+  const int cols = KDA ? c + 1 : c + 1 + N, ct = (cols + 3) / 4;
   for (int e0 = 0; e0 < (lay.rows / 4) * ct; e0 += kNT / 2) {
     const int e = e0 + tid / 2, part = tid & 1;
     const bool on = e < (lay.rows / 4) * ct;
@@ -203,10 +226,13 @@ __global__ void __launch_bounds__(kNT) decode_tree_kernel(const TreeParams p) {
     float acc[4][4] = {};
     if (on && (!M2 || r0 + 3 >= half)) {          // Mamba-2 reads the state with q alone
       const float* xr = xs + r0 * PK + 4 * part;
-      const float* ur = us + 4 * part;
+      const float* ur = xs + 4 * part;
       int at[4];
 #pragma unroll
-      for (int y = 0; y < 4; ++y) at[y] = (j0 + y <= c ? j0 + y : c) * PK;
+      for (int y = 0; y < 4; ++y) {
+        const int col = j0 + y < cols ? j0 + y : cols - 1;
+        at[y] = col <= c ? lay.us - lay.xs + col * PK : (col - c - 1) * PK;
+      }
 #pragma unroll 4
       for (int i = 0; i < dk; i += 8) {
         float4 u[4];
@@ -226,7 +252,23 @@ __global__ void __launch_bounds__(kNT) decode_tree_kernel(const TreeParams p) {
                                    acc[1][y] + __shfl_xor_sync(0xffffffffu, acc[1][y], 1),
                                    acc[2][y] + __shfl_xor_sync(0xffffffffu, acc[2][y], 1),
                                    acc[3][y] + __shfl_xor_sync(0xffffffffu, acc[3][y], 1));
-      if (on && part == (y & 1) && j0 + y <= c) st4(ys + (j0 + y) * lay.rows + r0, o);
+      if (on && part == (y & 1)) {
+        const int col = j0 + y;
+        if constexpr (KDA) {
+          if (col <= c) st4(ys + col * lay.rows + r0, o);
+        } else {
+          const int t = r0 < half ? r0 : r0 - half;      // (half is a multiple of 8)
+          if (col <= c) {
+            st4(ys + col * lay.rows + r0, mul4(o, ld4(&s_B[t])));
+          } else if (col < cols) {
+            float* m = (r0 < half ? kk : pp) + col - c - 1;
+            if (t < N) m[t * N] *= o.x;
+            if (t + 1 < N) m[(t + 1) * N] *= o.y;
+            if (t + 2 < N) m[(t + 2) * N] *= o.z;
+            if (t + 3 < N) m[(t + 3) * N] *= o.w;
+          }
+        }
+      }
     }
   }
   __syncthreads();
@@ -327,7 +369,7 @@ struct CommitParams {
 template <int FORM, typename TS>
 __global__ void __launch_bounds__(kNT) tree_commit_kernel(const CommitParams p) {
   constexpr bool KDA = FORM == SEED_KDA, M2 = FORM == SEED_MAMBA2;
-  __shared__ int s_path[SEED_MAX_NODES];
+  __shared__ int s_path[SEED_MAX_NODES], s_par[SEED_MAX_NODES];
   __shared__ float s_om[SEED_MAX_NODES], s_after[SEED_MAX_NODES + 1];
   __shared__ float s_red[2][kNT / 32];
   __shared__ int s_len;
@@ -338,11 +380,13 @@ __global__ void __launch_bounds__(kNT) tree_commit_kernel(const CommitParams p) 
   const int leaf = p.leaf[b];
   if (leaf < 0) return;
   const int c = p.ncols[unit];
+  if (tid < N) s_par[tid] = p.parent[(long long)b * N + tid];
+  __syncthreads();
   if (tid == 0) {
     int len = 0, u = leaf;
     bool ok = leaf < N;
     while (ok && u >= 0) {
-      const int up = p.parent[(long long)b * N + u];
+      const int up = s_par[u];
       if (up < -1 || up >= u) ok = false;
       s_path[len++] = u;
       u = up;
@@ -390,14 +434,23 @@ __global__ void __launch_bounds__(kNT) tree_commit_kernel(const CommitParams p) 
 
   bool bad = false;
   const bool on = tid < dk;
+  const float vbc = tid < dv ? vb[tid] : 0.f;      // d_k, d_v <= 128 threads
   float a = on ? p.a[unit * dk + tid] : 0.f;
   float P = KDA && on ? p.scale[unit * dk + tid] : 1.f;
   TS* U = static_cast<TS*>(p.U) + (unit * p.m + c) * (long long)dk;
   TS* V = static_cast<TS*>(p.V) + (unit * p.m + c) * (long long)dv;
-  for (int i = 0; i < len; ++i) {
+  float k_next = 0.f, al_next = 1.f, be_next = 0.f, w_next = 0.f;      // the next node's values (w: channel tid)
+  auto fetch = [&](int i) {
     const long long rt = row + (long long)s_path[i] * p.H;
-    const float k = on ? p.k[rt * dk + tid] : 0.f;
-    const float al = KDA ? (on ? p.alpha[rt * dk + tid] : 1.f) : p.alpha[rt];
+    if (on) k_next = p.k[rt * dk + tid];
+    if (!KDA || on) al_next = KDA ? p.alpha[rt * dk + tid] : p.alpha[rt];
+    be_next = p.beta[rt];
+    if (tid < dv) w_next = p.w[rt * dv + tid];
+  };
+  fetch(0);
+  for (int i = 0; i < len; ++i) {
+    const float k = k_next, al = al_next, be = be_next, w = w_next;
+    if (i + 1 < len) fetch(i + 1);
     a *= al;
     float ka = 0.f;
     if constexpr (!M2) {
@@ -408,7 +461,7 @@ __global__ void __launch_bounds__(kNT) tree_commit_kernel(const CommitParams p) 
 #pragma unroll
       for (int x = 0; x < kNT / 32; ++x) ka += s_red[i & 1][x];
     }
-    const float s = p.beta[rt] * (s_om[i] - ka);
+    const float s = be * (s_om[i] - ka);
     a = fmaf(s, k, a);
     if (on) {
       float u = k;
@@ -419,10 +472,10 @@ __global__ void __launch_bounds__(kNT) tree_commit_kernel(const CommitParams p) 
       bad = bad || !isfinite(fac_round<TS>(u));
       U[(long long)i * dk + tid] = fac_from_f<TS>(u);
     }
-    for (int e = tid; e < dv; e += kNT) {
-      const float x = fmaf(-s, vb[e], p.w[rt * dv + e]);
+    if (tid < dv) {
+      const float x = fmaf(-s, vbc, w);
       bad = bad || !isfinite(fac_round<TS>(x));
-      V[(long long)i * dv + e] = fac_from_f<TS>(x);
+      V[(long long)i * dv + tid] = fac_from_f<TS>(x);
     }
   }
   if (on) {
