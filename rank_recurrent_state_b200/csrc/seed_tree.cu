@@ -19,6 +19,7 @@
 // k_t . D_tj k_j, q_t . D_tj k_j and the decayed k_t, q_t for the product with the columns.
 // Then each thread owns a value channel and resolves the nodes in order.
 #include "seed_decode.cuh"
+#include "seed_tma.cuh"
 
 namespace seed {
 
@@ -45,19 +46,27 @@ struct TreeParams {
   int B, L, H, layer, m, slen, N, dk, dv;
 };
 
-// Shared-memory layout (floats).
+// Shared-memory layout (floats).  The stored V and the nodes' v are staged behind the rest
+// where at least two blocks then still share an SM: read where they are needed, they cost
+// the column phase a trip to memory every few columns (200 of 230 us of a batch of 3072
+// trees of 16 nodes were spent waiting).
 struct TreeSmem {
-  int rows, xs, us, ys, kk, pp, total;      // offsets; rows = 2 N rounded up to a multiple of 16
-  __host__ __device__ TreeSmem(int N, int m, int dk, int dv) {
+  int rows, xs, us, ys, kk, pp, vs, vv, total;      // offsets; rows = 2 N rounded up to a multiple of 16
+  bool staged;
+  __host__ __device__ TreeSmem(int N, int m, int dk, int dv, int elem_bytes) {
     rows = (2 * N + 15) & ~15;
     xs = 0;
-    us = xs + rows * (dk + 4);
-    const int u1 = ((m + 1 + 3) & ~3) * (dk + 4), w1 = N * dv;
+    us = xs + rows * (dk + 8);
+    const int u1 = ((m + 1 + 3) & ~3) * (dk + 8), w1 = N * dv;
     ys = us + (u1 > w1 ? u1 : w1);
-    const int y1 = (m + 1) * rows, k1 = N * (dk + 4);
+    const int y1 = (m + 1) * rows, k1 = N * (dk + 8);
     kk = ys + (y1 > k1 ? y1 : k1);
     pp = kk + N * N;
-    total = pp + N * N;
+    vs = (pp + N * N + 3) & ~3;
+    vv = vs + (m * dv * elem_bytes + 15) / 16 * 4;
+    total = vv + N * dv;
+    staged = total * 4 <= 112 * 1024;
+    if (!staged) total = vs;
   }
 };
 
@@ -68,9 +77,9 @@ __global__ void __launch_bounds__(kNT) decode_tree_kernel(const TreeParams p) {
   __shared__ int s_par[SEED_MAX_NODES];
   __shared__ __align__(16) float s_al[SEED_MAX_NODES], s_be[SEED_MAX_NODES], s_B[SEED_MAX_NODES];
   __shared__ unsigned long long s_anc[SEED_MAX_NODES];     // ancestors, the node itself left out
-  constexpr int dk = DK, dv = DV, PK = DK + 4, E = DK < 32 ? 1 : DK / 32;
+  constexpr int dk = DK, dv = DV, PK = DK + 8, E = DK < 32 ? 1 : DK / 32;
   const int N = p.N;
-  const TreeSmem lay(N, p.m, dk, dv);
+  const TreeSmem lay(N, p.m, dk, dv, sizeof(TS));
   float* xs = smf + lay.xs;      // rows t: k_t, rows rows/2 + t: q_t (KDA: decayed by B_t)
   float* us = smf + lay.us;      // true U columns, then a; later w
   float* ys = smf + lay.ys;      // KDA: the nodes' k; then [column][row]
@@ -86,6 +95,20 @@ __global__ void __launch_bounds__(kNT) decode_tree_kernel(const TreeParams p) {
     return;
   }
   const float* vb = p.vbar + ((long long)p.layer * p.H + h) * dv;
+
+  // ---- the columns of V and the nodes' v on their way
+  const TS* Vg = static_cast<const TS*>(p.V) + unit * (long long)p.m * dv;
+  TS* vs = reinterpret_cast<TS*>(smf + lay.vs);
+  float* vv = smf + lay.vv;
+  if (lay.staged) {
+    constexpr int per = 16 / (int)sizeof(TS);
+    for (int e = tid; e < c * dv / per; e += kNT) cp_async16(vs + e * per, Vg + e * per);
+    for (int e = tid; e < N * dv / 4; e += kNT) {
+      const int t = e / (dv / 4), i = 4 * (e % (dv / 4));
+      cp_async16(vv + t * dv + i, p.v + (((long long)b * N + t) * p.H + h) * dv + i);
+    }
+    cp_async_commit();
+  }
 
   // ---- the tree: s_par[t] = parent, or -2 for an unused node.  A node is used when
   // every step of its path goes to an earlier node and ends at -1.
@@ -127,14 +150,14 @@ __global__ void __launch_bounds__(kNT) decode_tree_kernel(const TreeParams p) {
       st4(ys + t * PK + i, ld4(p.k + (row + (long long)t * p.H) * dk + i));
     }
   } else {
-#pragma unroll 4
+#pragma unroll 8
     for (int e = tid; e < lay.rows * q4; e += kNT) {
       const int r = e / q4, i = 4 * (e % q4), t = r < half ? r : r - half;
       const float* src = r < half ? p.k : p.q;
       st4(xs + r * PK + i, t < N ? ld4(src + (row + (long long)t * p.H) * dk + i) : zero4());
     }
   }
-#pragma unroll 4
+#pragma unroll 8
   for (int e = tid; e < c * q4; e += kNT) {
     const int j = e / q4, i = 4 * (e % q4);
     float4 x = fac_ld4(U + (long long)j * dk + i);
@@ -217,14 +240,16 @@ __global__ void __launch_bounds__(kNT) decode_tree_kernel(const TreeParams p) {
   __syncthreads();
 
   // ---- ys[j][row] = x_row . (column j); column c is a, and with one decay per head the
-  // nodes' k follow.  Tiles of 4 rows x 4 columns, two lanes along the channels each.
+  // nodes' k follow.  Tiles of 4 rows (a quarter of the rows apart) x 4 columns, two lanes
+  // along the channels each: eight lanes then read 128 bytes of different banks.
+  const int rq = lay.rows / 4;
   const int cols = KDA ? c + 1 : c + 1 + N, ct = (cols + 3) / 4;
-  for (int e0 = 0; e0 < (lay.rows / 4) * ct; e0 += kNT / 2) {
+  for (int e0 = 0; e0 < rq * ct; e0 += kNT / 2) {
     const int e = e0 + tid / 2, part = tid & 1;
-    const bool on = e < (lay.rows / 4) * ct;
-    const int r0 = on ? 4 * (e % (lay.rows / 4)) : 0, j0 = on ? 4 * (e / (lay.rows / 4)) : 0;
+    const bool on = e < rq * ct;
+    const int r0 = on ? e % rq : 0, j0 = on ? 4 * (e / rq) : 0;
     float acc[4][4] = {};
-    if (on && (!M2 || r0 + 3 >= half)) {          // Mamba-2 reads the state with q alone
+    if (on) {
       const float* xr = xs + r0 * PK + 4 * part;
       const float* ur = xs + 4 * part;
       int at[4];
@@ -240,7 +265,8 @@ __global__ void __launch_bounds__(kNT) decode_tree_kernel(const TreeParams p) {
         for (int y = 0; y < 4; ++y) u[y] = ld4(ur + at[y] + i);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const float4 x = ld4(xr + r * PK + i);
+          if (M2 && r < 2) continue;          // Mamba-2 reads with q alone, rows from the half on
+          const float4 x = ld4(xr + r * rq * PK + i);
 #pragma unroll
           for (int y = 0; y < 4; ++y) acc[r][y] += dot4(x, u[y]);
         }
@@ -248,55 +274,43 @@ __global__ void __launch_bounds__(kNT) decode_tree_kernel(const TreeParams p) {
     }
 #pragma unroll
     for (int y = 0; y < 4; ++y) {
-      const float4 o = make_float4(acc[0][y] + __shfl_xor_sync(0xffffffffu, acc[0][y], 1),
-                                   acc[1][y] + __shfl_xor_sync(0xffffffffu, acc[1][y], 1),
-                                   acc[2][y] + __shfl_xor_sync(0xffffffffu, acc[2][y], 1),
-                                   acc[3][y] + __shfl_xor_sync(0xffffffffu, acc[3][y], 1));
-      if (on && part == (y & 1)) {
-        const int col = j0 + y;
-        if constexpr (KDA) {
-          if (col <= c) st4(ys + col * lay.rows + r0, o);
-        } else {
-          const int t = r0 < half ? r0 : r0 - half;      // (half is a multiple of 8)
-          if (col <= c) {
-            st4(ys + col * lay.rows + r0, mul4(o, ld4(&s_B[t])));
-          } else if (col < cols) {
-            float* m = (r0 < half ? kk : pp) + col - c - 1;
-            if (t < N) m[t * N] *= o.x;
-            if (t + 1 < N) m[(t + 1) * N] *= o.y;
-            if (t + 2 < N) m[(t + 2) * N] *= o.z;
-            if (t + 3 < N) m[(t + 3) * N] *= o.w;
-          }
+#pragma unroll
+      for (int r = 0; r < 4; ++r) acc[r][y] += __shfl_xor_sync(0xffffffffu, acc[r][y], 1);
+      const int col = j0 + y;
+      if (on && part == (y & 1) && col < cols) {
+#pragma unroll
+        for (int r = M2 ? 2 : 0; r < 4; ++r) {
+          const int row_ = r0 + r * rq, t = r0 + (r & 1) * rq;      // (2 rq = half)
+          if (col <= c) ys[col * lay.rows + row_] = KDA ? acc[r][y] : acc[r][y] * s_B[t];
+          else if (t < N) (r < 2 ? kk : pp)[t * N + col - c - 1] *= acc[r][y];
         }
       }
     }
   }
+  cp_async_wait<0>();
   __syncthreads();
 
   // ---- value channels: a thread resolves its channel's w and o, nodes in order
   float* ws = us;
   bool bad = false;
   for (int col = tid; col < dv; col += kNT) {
-    const TS* V = static_cast<const TS*>(p.V) + unit * (long long)p.m * dv + col;
+    const TS* V = (lay.staged ? vs : Vg) + col;
     const float vbc = vb[col];
     for (int t0 = 0; t0 < N; t0 += 8) {
       float rk[8], rq[8], vt[8];
 #pragma unroll
-      for (int r = 0; r < 8; ++r) vt[r] = t0 + r < N ? p.v[(row + (long long)(t0 + r) * p.H) * dv + col] : 0.f;
+      for (int r = 0; r < 8; ++r) {
+        vt[r] = 0.f;
+        if (t0 + r < N) vt[r] = lay.staged ? vv[(t0 + r) * dv + col] : p.v[(row + (long long)(t0 + r) * p.H) * dv + col];
+      }
 #pragma unroll
       for (int r = 0; r < 8; ++r) {
         rk[r] = vbc * ys[c * lay.rows + t0 + r];
         rq[r] = vbc * ys[c * lay.rows + half + t0 + r];
       }
-      for (int j0 = 0; j0 < c; j0 += 8) {
-       float vc[8];
-#pragma unroll
-       for (int x = 0; x < 8; ++x) vc[x] = fac_to_f(V[(long long)(j0 + x < c ? j0 + x : c - 1) * dv]);
-#pragma unroll
-       for (int x = 0; x < 8; ++x) {
-        if (j0 + x >= c) break;
-        const int j = j0 + x;
-        const float vj = vc[x];
+#pragma unroll 4
+      for (int j = 0; j < c; ++j) {
+        const float vj = fac_to_f(V[j * dv]);
         const float* y = ys + j * lay.rows + t0;
         if constexpr (!M2) {
           const float4 a0 = ld4(y), a1 = ld4(y + 4);
@@ -310,7 +324,6 @@ __global__ void __launch_bounds__(kNT) decode_tree_kernel(const TreeParams p) {
         rq[2] = fmaf(b0.z, vj, rq[2]); rq[3] = fmaf(b0.w, vj, rq[3]);
         rq[4] = fmaf(b1.x, vj, rq[4]); rq[5] = fmaf(b1.y, vj, rq[5]);
         rq[6] = fmaf(b1.z, vj, rq[6]); rq[7] = fmaf(b1.w, vj, rq[7]);
-       }
       }
 #pragma unroll
       for (int r = 0; r < 8; ++r) {
@@ -494,8 +507,8 @@ __global__ void __launch_bounds__(kNT) tree_commit_kernel(const CommitParams p) 
 template <int FORM, int DK, int DV, typename TS>
 int launch_tree_t(const TreeParams& p, cudaStream_t st) {
   static LaunchCache cache;
-  const size_t bytes = sizeof(float) * (size_t)TreeSmem(p.N, p.m, p.dk, p.dv).total;
-  constexpr size_t most = 220 * 1024;      // 64 nodes, 96 columns, d 128: 199 KB
+  const size_t bytes = sizeof(float) * (size_t)TreeSmem(p.N, p.m, p.dk, p.dv, sizeof(TS)).total;
+  constexpr size_t most = 220 * 1024;      // 64 nodes, 96 columns, d 128: 203 KB
   if (bytes > most) return SEED_ERR_SHAPE;
   int dev;
   if (int rc = cache.prepare(reinterpret_cast<const void*>(decode_tree_kernel<FORM, DK, DV, TS>), most, &dev)) return rc;
