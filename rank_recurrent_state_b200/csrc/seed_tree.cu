@@ -75,7 +75,7 @@ __global__ void __launch_bounds__(kNT) decode_tree_kernel(const TreeParams p) {
   constexpr bool KDA = FORM == SEED_KDA, M2 = FORM == SEED_MAMBA2;
   extern __shared__ __align__(16) float smf[];
   __shared__ int s_par[SEED_MAX_NODES];
-  __shared__ __align__(16) float s_al[SEED_MAX_NODES], s_be[SEED_MAX_NODES], s_B[SEED_MAX_NODES];
+  __shared__ __align__(16) float s_al[SEED_MAX_NODES], s_be[SEED_MAX_NODES], s_B[SEED_MAX_NODES], s_sc[SEED_MAX_COLS + 1];
   __shared__ unsigned long long s_anc[SEED_MAX_NODES];     // ancestors, the node itself left out
   constexpr int dk = DK, dv = DV, PK = DK + 8, E = DK < 32 ? 1 : DK / 32;
   const int N = p.N;
@@ -96,7 +96,26 @@ __global__ void __launch_bounds__(kNT) decode_tree_kernel(const TreeParams p) {
   }
   const float* vb = p.vbar + ((long long)p.layer * p.H + h) * dv;
 
-  // ---- the columns of V and the nodes' v on their way
+  // ---- q and k, the stored columns and the nodes' v on their way
+  const long long row = (long long)b * N * p.H + h;     // token t: row + t H
+  constexpr int q4 = dk / 4;
+  constexpr bool kRawU = !KDA && std::is_same<TS, float>::value;      // U's scales go to its dot products
+  float* const kt_rows = KDA ? ys : xs;                 // [t][PK]: the nodes' k
+  for (int e = tid; e < half * q4; e += kNT) {
+    const int t = e / q4, i = 4 * (e % q4);
+    const long long at = (row + (long long)t * p.H) * dk + i;
+    if (t < N) {
+      cp_async16(kt_rows + t * PK + i, p.k + at);
+      cp_async16(xs + (half + t) * PK + i, p.q + at);
+    } else {
+      if (!KDA) st4(xs + t * PK + i, zero4());
+      st4(xs + (half + t) * PK + i, zero4());
+    }
+  }
+  if constexpr (kRawU) {
+    const float* Ug = static_cast<const float*>(p.U) + unit * (long long)p.m * dk;
+    for (int e = tid; e < c * q4; e += kNT) cp_async16(us + (e / q4) * PK + 4 * (e % q4), Ug + 4 * e);
+  }
   const TS* Vg = static_cast<const TS*>(p.V) + unit * (long long)p.m * dv;
   TS* vs = reinterpret_cast<TS*>(smf + lay.vs);
   float* vv = smf + lay.vv;
@@ -107,8 +126,8 @@ __global__ void __launch_bounds__(kNT) decode_tree_kernel(const TreeParams p) {
       const int t = e / (dv / 4), i = 4 * (e % (dv / 4));
       cp_async16(vv + t * dv + i, p.v + (((long long)b * N + t) * p.H + h) * dv + i);
     }
-    cp_async_commit();
   }
+  cp_async_commit();
 
   // ---- the tree: s_par[t] = parent, or -2 for an unused node.  A node is used when
   // every step of its path goes to an earlier node and ends at -1.
@@ -141,33 +160,23 @@ __global__ void __launch_bounds__(kNT) decode_tree_kernel(const TreeParams p) {
   // ---- stored columns (true U) and a, beside them
   const TS* U = static_cast<const TS*>(p.U) + unit * (long long)p.m * dk;
   const float* sc = p.scale + unit * p.slen;
-  const long long row = (long long)b * N * p.H + h;     // token t: row + t H
-  constexpr int q4 = dk / 4;
-  if constexpr (KDA) {
-#pragma unroll 4
-    for (int e = tid; e < N * q4; e += kNT) {
-      const int t = e / q4, i = 4 * (e % q4);
-      st4(ys + t * PK + i, ld4(p.k + (row + (long long)t * p.H) * dk + i));
-    }
-  } else {
+  if constexpr (!kRawU) {
 #pragma unroll 8
-    for (int e = tid; e < lay.rows * q4; e += kNT) {
-      const int r = e / q4, i = 4 * (e % q4), t = r < half ? r : r - half;
-      const float* src = r < half ? p.k : p.q;
-      st4(xs + r * PK + i, t < N ? ld4(src + (row + (long long)t * p.H) * dk + i) : zero4());
+    for (int e = tid; e < c * q4; e += kNT) {
+      const int j = e / q4, i = 4 * (e % q4);
+      float4 x = fac_ld4(U + (long long)j * dk + i);
+      if constexpr (KDA) x = mul4(x, ld4(sc + i));
+      st4(us + j * PK + i, x);
     }
   }
-#pragma unroll 8
-  for (int e = tid; e < c * q4; e += kNT) {
-    const int j = e / q4, i = 4 * (e % q4);
-    float4 x = fac_ld4(U + (long long)j * dk + i);
-    if constexpr (KDA) x = mul4(x, ld4(sc + i));
-    else x = fma4(sc[j], x, zero4());
-    st4(us + j * PK + i, x);
+  if constexpr (!KDA) {
+    for (int j = tid; j < c; j += kNT) s_sc[j] = sc[j];
+    if (tid == 0) s_sc[c] = 1.f;      // a
   }
   for (int i = tid; i < dk; i += kNT) us[c * PK + i] = p.a[unit * dk + i];
   if (!KDA && tid < N) s_al[tid] = p.alpha[row + (long long)tid * p.H];
   if (tid < N) s_be[tid] = p.beta[row + (long long)tid * p.H];
+  cp_async_wait<0>();
   __syncthreads();
 
   // ---- paths
@@ -191,7 +200,7 @@ __global__ void __launch_bounds__(kNT) decode_tree_kernel(const TreeParams p) {
     for (int e = 0; e < E; ++e) {
       const int i = lane + 32 * e;
       kt[e] = used && i < dk ? ys[t * PK + i] : 0.f;
-      qt[e] = used && i < dk ? p.q[(row + (long long)t * p.H) * dk + i] : 0.f;
+      qt[e] = used && i < dk ? xs[(half + t) * PK + i] : 0.f;      // (decayed in place below)
       f[e] = 1.f;
     }
     // four nodes of the path at a time: their eight dot products are summed over the warp
@@ -281,13 +290,12 @@ __global__ void __launch_bounds__(kNT) decode_tree_kernel(const TreeParams p) {
 #pragma unroll
         for (int r = M2 ? 2 : 0; r < 4; ++r) {
           const int row_ = r0 + r * rq, t = r0 + (r & 1) * rq;      // (2 rq = half)
-          if (col <= c) ys[col * lay.rows + row_] = KDA ? acc[r][y] : acc[r][y] * s_B[t];
+          if (col <= c) ys[col * lay.rows + row_] = KDA ? acc[r][y] : acc[r][y] * (s_B[t] * s_sc[col]);
           else if (t < N) (r < 2 ? kk : pp)[t * N + col - c - 1] *= acc[r][y];
         }
       }
     }
   }
-  cp_async_wait<0>();
   __syncthreads();
 
   // ---- value channels: a thread resolves its channel's w and o, nodes in order
