@@ -49,6 +49,7 @@ size_t carve(ScanParams& p, const seed_scan_dims& d, bool backward, void* ws) {
 
 // Forward, or its recomputation: o, S_out, w and chunk_S where they are asked for.
 int forward(const ScanParams& p, const seed_scan_dims& d, cudaStream_t st) {
+  if (d.max_len <= 1 && d.tokens > 0 && p.chunk_S == nullptr) return launch_scan_one(p, d.form, st);
   if (!chunked(p, d)) return launch_scan_step(p, d.form, st);
   return with_factor_type_of(d.elem, [&](auto t) -> int {
     using T = decltype(t);

@@ -9,7 +9,9 @@ provides device memory and streams.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import functools
 from dataclasses import dataclass
 
 import torch
@@ -99,18 +101,23 @@ def _check(fn: str, rc: int) -> None:
         raise SeedError(fn, rc)
 
 
-def _check_state(dims: "Dims", state: "State") -> None:
-    """The C ABI sees only pointers: check here that the state's tensors have the
-    element types and sizes the dims describe (U and V in the factor format)."""
+@functools.lru_cache(maxsize=256)
+def _state_arrays(dims: "Dims") -> dict:
+    """Element type and least size of each state tensor."""
     B, L, H, m = dims.batch, dims.layers, dims.heads, dims.m
     slen = dims.d_k if dims.form == SEED_KDA else (m + 3) // 4 * 4
-    want = {"a": (torch.float32, B * L * H * dims.d_k),
+    return {"a": (torch.float32, B * L * H * dims.d_k),
             "U": (FACTOR_DTYPES[dims.factors], B * L * H * m * dims.d_k),
             "V": (FACTOR_DTYPES[dims.factors], B * L * H * m * dims.d_v),
             "scale": (torch.float32, B * L * H * slen),
             "ncols": (torch.int32, B * L * H),
             "vbar": (torch.float32, L * H * dims.d_v)}
-    for name, (dtype, n) in want.items():
+
+
+def _check_state(dims: "Dims", state: "State") -> None:
+    """The C ABI sees only pointers: check here that the state's tensors have the
+    element types and sizes the dims describe (U and V in the factor format)."""
+    for name, (dtype, n) in _state_arrays(dims).items():
         t = getattr(state, name)
         if t.dtype != dtype or t.numel() < n:
             raise ValueError(f"state.{name}: expected {dtype} with at least {n} elements, got {t.dtype} "
@@ -328,18 +335,25 @@ class ScanWorkspace:
         return self.buf.data_ptr()
 
 
-def _check_arrays(where: torch.device, **arrays) -> None:
-    """The C ABI sees only pointers: every array (name=(tensor, dtype, elements); None is
+def _check_arrays(where: torch.device, specs: dict, **arrays) -> None:
+    """The C ABI sees only pointers: every array (name=(tensor, its entry of specs); None is
     an absent optional one) has its element type, its size, and lies on `where`."""
-    for name, (t, dtype, n) in arrays.items():
+    for name, (t, spec) in arrays.items():
         if t is None:
             continue
+        dtype, n = specs[spec]
         if t.dtype != dtype or t.numel() != n:
             raise ValueError(f"{name}: expected {dtype} with {n} elements, got {t.dtype} with {t.numel()}")
         if t.device != where:
             raise ValueError(f"{name}: on {t.device}, the workspace on {where}")
 
 
+def _on(device: torch.device):
+    """The context in which a call launches: `device` current, whichever was before."""
+    return contextlib.nullcontext() if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+
+
+@functools.lru_cache(maxsize=256)
 def _scan_arrays(d: ScanDims) -> dict:
     qk, v, g = d.tokens * d.k_heads * d.d_k, d.tokens * d.heads * d.d_v, d.tokens * d.heads
     f32 = torch.float32
@@ -351,12 +365,10 @@ def _scan_arrays(d: ScanDims) -> dict:
 def seed_dense_scan(dims: ScanDims, offsets, q, k, v, alpha, beta, o, ws: ScanWorkspace,
                     S0: torch.Tensor | None = None, S_out: torch.Tensor | None = None, stream=None) -> None:
     """The dense recurrence over packed sequences; offsets int32 [seqs + 1] on the device."""
-    a = _scan_arrays(dims)
-    _check_arrays(ws.buf.device, offsets=(offsets, *a["offsets"]), q=(q, *a["qk"]), k=(k, *a["qk"]), v=(v, *a["v"]),
-                  alpha=(alpha, *a["alpha"]), beta=(beta, *a["beta"]), o=(o, *a["v"]), S0=(S0, *a["S"]),
-                  S_out=(S_out, *a["S"]))
+    _check_arrays(ws.buf.device, _scan_arrays(dims), offsets=(offsets, "offsets"), q=(q, "qk"), k=(k, "qk"), v=(v, "v"),
+                  alpha=(alpha, "alpha"), beta=(beta, "beta"), o=(o, "v"), S0=(S0, "S"), S_out=(S_out, "S"))
     d = dims.c()
-    with torch.cuda.device(ws.buf.device):
+    with _on(ws.buf.device):
         _check("seed_dense_scan", _lib.load().seed_dense_scan(
             ctypes.byref(d), _ptr(offsets), _ptr(q), _ptr(k), _ptr(v), _ptr(alpha), _ptr(beta), _ptr(S0), _ptr(o),
             _ptr(S_out), ws.ptr, ws.nbytes, _stream(stream)))
@@ -366,13 +378,12 @@ def seed_dense_scan_backward(dims: ScanDims, offsets, q, k, v, alpha, beta, d_o,
                              ws: ScanWorkspace, S0: torch.Tensor | None = None, dS_out: torch.Tensor | None = None,
                              dS0: torch.Tensor | None = None, stream=None) -> None:
     """Gradients of seed_dense_scan into dq, dk, dv, dlog_alpha, dbeta and dS0 (see seed.h)."""
-    a = _scan_arrays(dims)
-    _check_arrays(ws.buf.device, offsets=(offsets, *a["offsets"]), q=(q, *a["qk"]), k=(k, *a["qk"]), v=(v, *a["v"]),
-                  alpha=(alpha, *a["alpha"]), beta=(beta, *a["beta"]), d_o=(d_o, *a["v"]), dq=(dq, *a["qk"]),
-                  dk=(dk, *a["qk"]), dv=(dv, *a["v"]), dlog_alpha=(dlog_alpha, *a["alpha"]),
-                  dbeta=(dbeta, *a["beta"]), S0=(S0, *a["S"]), dS_out=(dS_out, *a["S"]), dS0=(dS0, *a["S"]))
+    _check_arrays(ws.buf.device, _scan_arrays(dims), offsets=(offsets, "offsets"), q=(q, "qk"), k=(k, "qk"), v=(v, "v"),
+                  alpha=(alpha, "alpha"), beta=(beta, "beta"), d_o=(d_o, "v"), dq=(dq, "qk"), dk=(dk, "qk"),
+                  dv=(dv, "v"), dlog_alpha=(dlog_alpha, "alpha"), dbeta=(dbeta, "beta"), S0=(S0, "S"),
+                  dS_out=(dS_out, "S"), dS0=(dS0, "S"))
     d = dims.c()
-    with torch.cuda.device(ws.buf.device):
+    with _on(ws.buf.device):
         _check("seed_dense_scan_backward", _lib.load().seed_dense_scan_backward(
             ctypes.byref(d), _ptr(offsets), _ptr(q), _ptr(k), _ptr(v), _ptr(alpha), _ptr(beta), _ptr(d_o), _ptr(S0),
             _ptr(dS_out), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dlog_alpha), _ptr(dbeta), _ptr(dS0), ws.ptr, ws.nbytes,
@@ -381,25 +392,31 @@ def seed_dense_scan_backward(dims: ScanDims, offsets, q, k, v, alpha, beta, d_o,
 
 # ------------------------------------------------------------------ drafted tokens
 
-def _tree_arrays(dims: Dims, parent: torch.Tensor) -> tuple:
-    if parent.dim() != 2 or parent.shape[0] != dims.batch:
-        raise ValueError(f"parent: expected [{dims.batch}][nodes], got {tuple(parent.shape)}")
-    n = int(parent.shape[1])
+@functools.lru_cache(maxsize=256)
+def _tree_arrays(dims: Dims, n: int) -> dict:
     g = dims.batch * n * dims.heads
     f32 = torch.float32
-    return n, {"parent": (torch.int32, dims.batch * n), "k": (f32, g * dims.d_k), "v": (f32, g * dims.d_v),
-               "alpha": (f32, g * dims.d_k if dims.form == SEED_KDA else g), "beta": (f32, g)}
+    return {"parent": (torch.int32, dims.batch * n), "leaf": (torch.int32, dims.batch), "k": (f32, g * dims.d_k),
+            "v": (f32, g * dims.d_v), "alpha": (f32, g * dims.d_k if dims.form == SEED_KDA else g), "beta": (f32, g)}
+
+
+def _tree_nodes(dims: Dims, state: State, parent: torch.Tensor, ws: Workspace) -> int:
+    _check_state(dims, state)
+    if state.U.device != ws.buf.device:
+        raise ValueError(f"state: on {state.U.device}, the workspace on {ws.buf.device}")
+    if parent.dim() != 2 or parent.shape[0] != dims.batch:
+        raise ValueError(f"parent: expected [{dims.batch}][nodes], got {tuple(parent.shape)}")
+    return int(parent.shape[1])
 
 
 def seed_decode_tree(dims: Dims, state: State, layer: int, parent, q, k, v, alpha, beta, o, w, ws: Workspace,
                      stream=None) -> None:
     """Read a tree of drafted tokens against the stored state: parent [B][N] int32 (see seed.h)."""
-    _check_state(dims, state)
-    n, a = _tree_arrays(dims, parent)
-    _check_arrays(ws.buf.device, parent=(parent, *a["parent"]), q=(q, *a["k"]), k=(k, *a["k"]), v=(v, *a["v"]),
-                  alpha=(alpha, *a["alpha"]), beta=(beta, *a["beta"]), o=(o, *a["v"]), w=(w, *a["v"]))
+    n = _tree_nodes(dims, state, parent, ws)
+    _check_arrays(ws.buf.device, _tree_arrays(dims, n), parent=(parent, "parent"), q=(q, "k"), k=(k, "k"), v=(v, "v"),
+                  alpha=(alpha, "alpha"), beta=(beta, "beta"), o=(o, "v"), w=(w, "v"))
     d, s = dims.c(), state.c()
-    with torch.cuda.device(ws.buf.device):
+    with _on(ws.buf.device):
         _check("seed_decode_tree", _lib.load().seed_decode_tree(
             ctypes.byref(d), ctypes.byref(s), layer, n, _ptr(parent), _ptr(q), _ptr(k), _ptr(v), _ptr(alpha),
             _ptr(beta), _ptr(o), _ptr(w), ws.ptr, ws.nbytes, _stream(stream)))
@@ -408,12 +425,11 @@ def seed_decode_tree(dims: Dims, state: State, layer: int, parent, q, k, v, alph
 def seed_decode_tree_commit(dims: Dims, state: State, layer: int, parent, leaf, k, v, alpha, beta, w, ws: Workspace,
                             stream=None) -> None:
     """Append the path to node leaf[b] (int32 [B]; negative: none) to the stored state."""
-    _check_state(dims, state)
-    n, a = _tree_arrays(dims, parent)
-    _check_arrays(ws.buf.device, parent=(parent, *a["parent"]), leaf=(leaf, torch.int32, dims.batch), k=(k, *a["k"]),
-                  v=(v, *a["v"]), alpha=(alpha, *a["alpha"]), beta=(beta, *a["beta"]), w=(w, *a["v"]))
+    n = _tree_nodes(dims, state, parent, ws)
+    _check_arrays(ws.buf.device, _tree_arrays(dims, n), parent=(parent, "parent"), leaf=(leaf, "leaf"), k=(k, "k"),
+                  v=(v, "v"), alpha=(alpha, "alpha"), beta=(beta, "beta"), w=(w, "v"))
     d, s = dims.c(), state.c()
-    with torch.cuda.device(ws.buf.device):
+    with _on(ws.buf.device):
         _check("seed_decode_tree_commit", _lib.load().seed_decode_tree_commit(
             ctypes.byref(d), ctypes.byref(s), layer, n, _ptr(parent), _ptr(leaf), _ptr(k), _ptr(v), _ptr(alpha),
             _ptr(beta), _ptr(w), ws.ptr, ws.nbytes, _stream(stream)))
