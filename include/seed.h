@@ -331,7 +331,11 @@ int seed_dense_scan(const seed_scan_dims* dims, const int32_t* offsets, const vo
  *   of the terms it sums, not of a small difference of theirs), and
  *   dS0 [seqs][heads][d_k][d_v] float32, or NULL; may be dS_out itself.
  * The forward's states are recomputed; nothing is kept from the forward call.  Results
- * do not depend on the order in which blocks run (no atomic sums).                   */
+ * do not depend on the order in which blocks run (no atomic sums).
+ * In both calls a sequence with non-finite inputs has unspecified results, from up to 63
+ * tokens before the first of them; other sequences are not touched by it.  The forward
+ * call raises SEED_FLAG_NONFINITE for it.  SEED_FLAG_TIMEOUT: a bounded wait inside a block
+ * gave up; the results of that (sequence, head) are unspecified.                     */
 int seed_dense_scan_backward(const seed_scan_dims* dims, const int32_t* offsets, const void* q,
                              const void* k, const void* v, const float* alpha, const float* beta,
                              const void* d_o, const float* S0, const float* dS_out, void* dq, void* dk,
@@ -390,7 +394,8 @@ int seed_get_diagnostics(void* ws, void* stream, uint32_t* counters);
  * the units it had not finished are left unchanged (a decode warp fails on its
  * first unit, before touching any unit; a compression block's unit goes to the
  * Householder path as usual).  enable = 0 turns it off; seed_workspace_init clears
- * it.  The workspace word lies past the status word and the counters.              */
+ * it.  The workspace word lies past the status word and the counters.  (The scans'
+ * passes have bounded waits too, but not this hook.)                                 */
 int seed_debug_wait_fault(void* ws, size_t ws_bytes, int32_t enable, void* stream);
 
 /* Static description of a seed_status code. */

@@ -20,12 +20,23 @@ struct Carver {
   }
 };
 
-// The chunked passes take d_k and d_v of 64 and 128 from kStepMost tokens on; shorter
-// sequences and smaller heads go token by token.
-constexpr int kStepMost = 32;
-bool chunked(const ScanParams& p, const seed_scan_dims& d) {
-  return p.dk >= 64 && p.dv >= 64 && d.max_len > kStepMost;
+// The chunked kernels take d_k and d_v of 64 and 128; sequences up to step_most tokens, and
+// smaller heads, go token by token.  The chunked kernels cost a whole chunk however short
+// it is, the token-by-token ones a fixed time per token and, once their blocks fill the
+// SMs, work per token and head.  Measured (us, 128 x 128 bf16, forward; step / chunked): GDN 48
+// heads 32 tokens 42 / 44, 48 tokens 51 / 44; 768 heads 8 tokens 101 / 134, 16 tokens 163 /
+// 139.  KDA, whose chunks cost more to prepare: 48 heads 48 tokens 51 / 55, 64 tokens 61 /
+// 56; 768 heads 16 tokens 171 / 244, 32 tokens 292 / 254.  (Backward: the same crossings.)
+int step_most(const seed_scan_dims& d) {
+  const bool many = (long long)d.seqs * d.heads >= 2 * 148, kda = d.form == SEED_KDA;
+  return many ? (kda ? 24 : 10) : (kda ? 48 : 32);
 }
+bool chunked(const ScanParams& p, const seed_scan_dims& d) {
+  return p.dk >= 64 && p.dv >= 64 && d.max_len > step_most(d);
+}
+// One or two tokens per sequence: the kernel that reads the states in whole rows (768 heads,
+// one token 36 us against 64 token by token, two tokens 42 against 69, eight 110 against 101).
+constexpr int kOneMost = 2;
 
 // Assigns the scratch pointers (null base: only counts) and returns the bytes used.
 size_t carve(ScanParams& p, const seed_scan_dims& d, bool backward, void* ws) {
@@ -49,7 +60,7 @@ size_t carve(ScanParams& p, const seed_scan_dims& d, bool backward, void* ws) {
 
 // Forward, or its recomputation: o, S_out, w and chunk_S where they are asked for.
 int forward(const ScanParams& p, const seed_scan_dims& d, cudaStream_t st) {
-  if (d.max_len <= 1 && d.tokens > 0 && p.chunk_S == nullptr) return launch_scan_one(p, d.form, st);
+  if (d.max_len <= kOneMost && d.tokens > 0 && p.chunk_S == nullptr) return launch_scan_one(p, d.form, st);
   if (!chunked(p, d)) return launch_scan_step(p, d.form, st);
   return with_factor_type_of(d.elem, [&](auto t) -> int {
     using T = decltype(t);

@@ -213,7 +213,7 @@ SEED_DEV bool chunk_at(const ScanParams& p, int slot, ChunkAt* c) {
 }
 
 // ------------------------------------------------------------------ launchers
-// One token per sequence, forward only (seed_scan_one.cu).
+// One or two tokens per sequence, forward only (seed_scan_one.cu).
 int launch_scan_one(const ScanParams& p, int form, cudaStream_t st);
 // Token-by-token kernels (seed_scan_step.cu).
 int launch_scan_step(const ScanParams& p, int form, cudaStream_t st);

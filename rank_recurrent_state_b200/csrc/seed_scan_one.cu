@@ -1,13 +1,13 @@
-// seed_scan_one.cu -- the scan for one token per sequence: a model served with dense
-// states takes it every decode step.
+// seed_scan_one.cu -- the scan for one or two tokens per sequence: a model served with
+// dense states takes it every decode step.
 //
 // Bound by the states' bytes: a block holds the whole d_k x d_v state of one (sequence,
 // head) in registers, read and written once in float4 rows (coalesced, streaming), and
 // forms S^T k and S^T q together before the update, as the dense step does:
 //     w = beta (v - S'^T k), S+ = S' + k w^T, o = S'^T q + (k . q) w
-// Longer sequences take a block-wide reduction per token; the token-by-token kernel, whose
-// columns need none but whose accesses to the state are 32-byte pieces, is faster from two
-// tokens on (one token for 16 x 48 heads of 128 x 128: 46 us there).
+// One token of 16 sequences x 48 heads of 128 x 128: 20 us, 5.1 TB/s (the token-by-token
+// kernel, whose accesses to the state are 32-byte pieces, 46 us).  Every token costs two
+// block-wide barriers, so longer sequences go to the kernels without them.
 #include "seed_scan.cuh"
 
 namespace seed {

@@ -344,3 +344,69 @@ def test_float32_results_are_float32_accurate():
     for t in range(0, 1500, 64):
         r = ref["o"][t:t + 64]
         assert np.linalg.norm(o[t:t + 64] - r) <= (F32 + eps) * np.linalg.norm(r), t
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("hint", [1, 2, 20, 1000])
+def test_max_len_decides_speed_alone(form, hint):
+    """Sequences longer and shorter than the hint: every kernel takes every length."""
+    from dataclasses import replace
+    p = Problem(form, [3, 70, 0, 130, 1], 4, 2, 128, 64, "f16", seed=17)
+    p.dims = replace(p.dims, max_len=hint)
+    p.ws = p.S.ScanWorkspace(p.dims, backward=True)
+    out = p.outputs()
+    p.forward(out)
+    p.backward(out)
+    assert p.S.seed_get_status(p.ws) == 0
+    p.check(out)
+
+
+@pytest.mark.parametrize("form", FORMS)
+def test_many_sequences_and_heads(form):
+    """More (sequence, head) pairs than SMs, more sequences than one probe of the chunk
+    look-up, lengths around the switch between the kernels."""
+    rng = np.random.default_rng(18)
+    lens = rng.integers(0, 30, size=70).tolist()
+    p = Problem(form, lens, 6, 3, 64, 64, "bf16", seed=18)
+    out = p.outputs()
+    p.forward(out)
+    p.backward(out)
+    assert p.S.seed_get_status(p.ws) == 0
+    p.check(out)
+
+
+def test_arrays_beyond_32_bit_elements():
+    """v and o of more than 2^31 elements: the last sequence equals a call of its own."""
+    from rank_recurrent_state_b200 import seed as S
+    h, d, n, tail = 64, 128, 262400, 150
+    g = torch.Generator(device="cuda").manual_seed(19)
+    k = torch.randn(n, 1, d, generator=g, device="cuda")
+    k = (k / k.norm(dim=-1, keepdim=True)).bfloat16()
+    v = torch.empty(n, h, d, device="cuda", dtype=torch.bfloat16).normal_(generator=g)
+    alpha = torch.rand(n, h, generator=g, device="cuda") * 0.1 + 0.9
+    beta = torch.rand(n, h, generator=g, device="cuda")
+    assert v.numel() > 2 ** 31
+    o = torch.empty_like(v)
+    off = torch.tensor([0, n - tail, n], dtype=torch.int32, device="cuda")
+    dims = S.ScanDims(S.SEED_GDN, 2, n, h, 1, d, d, n, S.SEED_FACTORS_BF16)
+    ws = S.ScanWorkspace(dims)
+    S_out = torch.empty(2, h, d, d, device="cuda")
+    S.seed_dense_scan(dims, off, k, k, v, alpha, beta, o, ws, S_out=S_out)
+    assert S.seed_get_status(ws) == 0
+    one = S.ScanDims(S.SEED_GDN, 1, tail, h, 1, d, d, tail, S.SEED_FACTORS_BF16)
+    x = [t[n - tail:].contiguous() for t in (k, k, v, alpha, beta)]
+    o1, S1 = torch.empty_like(x[2]), torch.empty(1, h, d, d, device="cuda")
+    S.seed_dense_scan(one, torch.tensor([0, tail], dtype=torch.int32, device="cuda"), *x, o1, S.ScanWorkspace(one), S_out=S1)
+    assert torch.equal(o[n - tail:], o1) and torch.equal(S_out[1], S1[0])
+
+
+def test_the_binding_refuses_strided_and_foreign_arrays():
+    p = Problem("gdn", [20], 2, 2, 64, 64, "f32", seed=20)
+    out = p.outputs()
+    p.x["v"] = torch.stack([p.x["v"], p.x["v"]], -1)[..., 0]
+    with pytest.raises(ValueError, match="contiguous"):
+        p.forward(out)
+    p.x["v"] = p.x["v"].contiguous().cpu()
+    with pytest.raises(ValueError, match="v: on cpu"):
+        p.forward(out)
+    assert torch.isnan(out["o"]).all()
