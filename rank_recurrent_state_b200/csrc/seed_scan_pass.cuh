@@ -100,8 +100,10 @@ SEED_DEV void pass_wait(uint64_t* bar, uint32_t phase, volatile int* dead, uint3
 }
 
 // The products of a two-term A operand in tensor memory (the second term a_lo columns
-// behind) with a tile (its descriptor; a second term b_lo bytes behind): hi hi, lo hi and,
-// for a tile of two terms, hi lo.  KS steps of 16, step(ks) bytes apart in the tile.
+// behind) with a tile (its descriptor; a second term b_lo bytes behind): lo hi, for a tile
+// of two terms hi lo, and hi hi last.  The accumulator rounds towards zero at every step,
+// so the small products go first, while it is small (errors of 1.3e-6 of the result with
+// hi hi first).  KS steps of 16, step(ks) bytes apart in the tile.
 template <int KS, bool TWO, uint32_t IDESC, typename Step>
 SEED_DEV void product(uint32_t d, uint32_t a, uint32_t a_lo, uint64_t tile, uint32_t b_lo, bool accumulate, Step step) {
   const uint64_t high = tile & 0xffffffff00000000ull;
@@ -111,7 +113,7 @@ SEED_DEV void product(uint32_t d, uint32_t a, uint32_t a_lo, uint64_t tile, uint
   for (int t = 0; t < (TWO ? 3 : 2); ++t) {
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks)
-      umma_ts(d, a + (t == 1 ? a_lo : 0u) + 8 * ks, high | (low + (((t == 2 ? b_lo : 0u) + step(ks)) >> 4)), IDESC,
+      umma_ts(d, a + (t == 0 ? a_lo : 0u) + 8 * ks, high | (low + (((TWO && t == 1 ? b_lo : 0u) + step(ks)) >> 4)), IDESC,
               accumulate || t + ks > 0);
   }
 }
@@ -123,7 +125,7 @@ SEED_DEV void product_ss(uint32_t d, uint64_t a, uint32_t a_lo, StepA step_a, ui
   for (int t = 0; t < 3; ++t) {
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks)
-      umma_ss(d, a + (((t == 1 ? a_lo : 0u) + step_a(ks)) >> 4), b + (((t == 2 ? b_lo : 0u) + step_b(ks)) >> 4), IDESC,
+      umma_ss(d, a + (((t == 0 ? a_lo : 0u) + step_a(ks)) >> 4), b + (((t == 1 ? b_lo : 0u) + step_b(ks)) >> 4), IDESC,
               t + ks > 0);
   }
 }
