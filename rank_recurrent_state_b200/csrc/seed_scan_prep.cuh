@@ -82,8 +82,13 @@ SEED_DEV void gram_tile(float (&c)[4], const S* X, const S* Y, const float* m, i
     const float* x0 = X + (r0 + g) * PK + t;
     const float* x1 = x0 + 8 * PK;
     const float* y0 = Y + (n0 + g) * PK + t;
-#pragma unroll 4
-    for (int k = 0; k < DK; k += 8) {
+    // Accumulators round towards zero at every step: the small products have one of their
+    // own, the others one for each quarter of the channels, added to nearest at the end.
+    float lo[4] = {}, hi[4][4] = {};
+#pragma unroll
+    for (int k4 = 0; k4 < 4; ++k4)
+#pragma unroll
+    for (int k = k4 * (DK / 4); k < (k4 + 1) * (DK / 4); k += 8) {
       const float a[4] = {x0[k], x1[k], x0[k + 4], x1[k + 4]};
       float b[2] = {y0[k], y0[k + 4]};
       if (m != nullptr) {
@@ -94,10 +99,12 @@ SEED_DEV void gram_tile(float (&c)[4], const S* X, const S* Y, const float* m, i
       const float al[4] = {a[0] - ah[0], a[1] - ah[1], a[2] - ah[2], a[3] - ah[3]};
       const float bh[2] = {tf32_hi(b[0]), tf32_hi(b[1])};
       const float bl[2] = {b[0] - bh[0], b[1] - bh[1]};
-      mma_tf32(c, al, bh);
-      mma_tf32(c, ah, bl);
-      mma_tf32(c, ah, bh);
+      mma_tf32(lo, al, bh);
+      mma_tf32(lo, ah, bl);
+      mma_tf32(hi[k4], ah, bh);
     }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) c[e] = ((hi[0][e] + hi[1][e]) + (hi[2][e] + hi[3][e])) + lo[e];
   } else {
     const S* x0 = X + (r0 + g) * PK + 2 * t;
     const S* x1 = x0 + 8 * PK;

@@ -3,7 +3,7 @@
 //
 // A float32 product on the tensor cores: each operand is scaled by a power of two (per
 // row, so that the row's largest value lies in [1, 2)), split as x = hi + lo in fp16,
-// and multiplied as hi hi + hi lo + lo hi with float32 accumulation.  hi is off by at
+// and multiplied as lo hi + hi lo + hi hi with float32 accumulation.  hi is off by at
 // most 2^-11 of the row's scale, lo by 2^-25 (fp16's subnormal step is 2^-24), and the
 // dropped lo lo is below 2^-22: the products are accurate to about 2^-22 of the rows'
 // scales, as float32 FMA chains are, at a third of the fp16 rate.  Scaling and its
