@@ -109,19 +109,39 @@ SEED_DEV void grad_sums(const ScanParams& p, const ChunkAt& ck, int h, Sm& sm, f
         if constexpr (!M2) sh[a] = fmaf(sm.xy.Y[(i0 + b) * PX + i0 + a], t, sh[a]);
       }
     }
-    // columns i0 .. i0+3 against rows m >= i0+3, then the few inside the block
+    // columns i0 .. i0+3 against row i0+3, then four rows behind it at a time (their X and
+    // Y are one float4 per column), then the few inside the block
     float sc[4] = {};
     f = 1.f;
-#pragma unroll 4
-    for (int m = i0 + 3; m < kChunk; ++m) {
-      const float tq = f * sm.q[m * PK + c];
-      const float tk = M2 ? 0.f : -f * sm.beta[m] * sm.k[m * PK + c];
+    {
+      const float tq = sm.q[(i0 + 3) * PK + c];
+      const float tk = M2 ? 0.f : -sm.beta[i0 + 3] * sm.k[(i0 + 3) * PK + c];
+#pragma unroll
+      for (int a = 0; a < 3; ++a) {
+        sc[a] = sm.xy.X[(i0 + a) * PX + i0 + 3] * tq;
+        if constexpr (!M2) sc[a] = fmaf(sm.xy.Y[(i0 + a) * PX + i0 + 3], tk, sc[a]);
+      }
+    }
+#pragma unroll 1
+    for (int m = i0 + 4; m < kChunk; m += 4) {
+      float4 x[4], y[4];
 #pragma unroll
       for (int a = 0; a < 4; ++a) {
-        sc[a] = fmaf(sm.xy.X[(i0 + a) * PX + m], tq, sc[a]);
-        if constexpr (!M2) sc[a] = fmaf(sm.xy.Y[(i0 + a) * PX + m], tk, sc[a]);
+        x[a] = ld4(&sm.xy.X[(i0 + a) * PX + m]);
+        if constexpr (!M2) y[a] = ld4(&sm.xy.Y[(i0 + a) * PX + m]);
       }
-      if (m + 1 < kChunk) f *= dec(m + 1);
+      const float4 be4 = ld4(&sm.beta[m]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        f *= dec(m + e);
+        const float tq = f * sm.q[(m + e) * PK + c];
+        const float tk = M2 ? 0.f : -f * (&be4.x)[e] * sm.k[(m + e) * PK + c];
+#pragma unroll
+        for (int a = 0; a < 4; ++a) {
+          sc[a] = fmaf((&x[a].x)[e], tq, sc[a]);
+          if constexpr (!M2) sc[a] = fmaf((&y[a].x)[e], tk, sc[a]);
+        }
+      }
     }
     const float br[4] = {d1 * d2 * d3, d2 * d3, d3, 1.f};     // D between column i0 + a and row i0 + 3
     float vs[4], kh[4], last[4];
