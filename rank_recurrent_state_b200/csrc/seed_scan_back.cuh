@@ -13,7 +13,9 @@
 //
 // Warps 0-7 own the lanes, a thread of warp 8 issues the products, one of warp 9 copies.
 // The chain per chunk is dS -> x -> dw -> dS; do^T P does not depend on it.  Waits are
-// bounded as in the forward pass.
+// bounded as in the forward pass.  Measured: GDN, 6 documents of up to 1500 tokens x 16
+// heads, 235 us (24 chunks in turn, 10 us each; token by token 826 us).  Bound by latency:
+// two more conversions than the forward pass, and dw and dS stored a value at a time.
 #pragma once
 
 #include "seed_scan_pass.cuh"

