@@ -314,9 +314,9 @@ size_t seed_scan_workspace_bytes(const seed_scan_dims* dims, int32_t backward);
  *   alpha   [tokens][heads], KDA [tokens][heads][d_k]          beta [tokens][heads]
  *   S0      [seqs][heads][d_k][d_v] float32, or NULL for zeros
  *   S_out   the same, or NULL: the states behind the last tokens; may be S0 itself
- * alpha and beta are float32.  Decays enter as products (never as quotients or
- * logarithms), so any finite alpha is allowed, zero included.  All states and sums are
- * float32; o is rounded once.  With d_k and d_v from the other calls, S_out is one
+ * alpha and beta are float32.  Decays enter as products over up to 64 tokens (never as
+ * quotients or logarithms), so any finite alpha whose products do not overflow is allowed,
+ * zero included.  All states and sums are float32; o is rounded once.  With d_k and d_v from the other calls, S_out is one
  * layer's S_dense for seed_state_init_from_dense.                                   */
 int seed_dense_scan(const seed_scan_dims* dims, const int32_t* offsets, const void* q, const void* k,
                     const void* v, const float* alpha, const float* beta, const float* S0, void* o,
